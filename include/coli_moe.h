@@ -32,7 +32,7 @@
  *    COLI_E_* code is returned.  A failed launch returns COLI_E_HIP; a fault
  *    inside a kernel surfaces at the caller's next synchronisation.
  *  - Results are deterministic: the same inputs give bit-identical outputs on
- *    every run (no floating-point atomics anywhere).
+ *    every run (no floating-point atomics on device memory).
  *  - Calls that share a workspace or route buffer must not overlap in time.
  */
 #ifndef COLI_MOE_H
@@ -401,6 +401,137 @@ int coli_moe_mx_dots(const coli_moe_layer_t *layer, int32_t expert, int32_t matr
                      const uint8_t *q_act, const uint8_t *e_act, int32_t T, float *out,
                      void *stream);
 
+/* ---- one projection with the adapters of many requests ---------------------
+ * A batch of T rows holds n_requests requests; request i covers rows
+ * offsets[i] .. offsets[i+1] and brings its own low-rank adapter beside the
+ * matrix that all of them share (in serving, one token per request in decode
+ * and a prompt per request in prefill; in training, one sequence each).
+ *  offsets [n_requests+1] int32, ascending, within [0, T]; empty requests are
+ *          allowed, and rows before the first or behind the last request.
+ *  adapter [n_requests] int32: an index into the adapter tables; any value
+ *          outside [0, n_adapters) means no adapter.  Several requests may
+ *          name the same one.
+ *  1 <= n_requests <= 65536. */
+typedef struct coli_moe_requests {
+  int32_t n_requests;
+  const int32_t *offsets; /* device */
+  const int32_t *adapter; /* device */
+} coli_moe_requests_t;
+
+/* Tables of low-rank adapters of one N x K matrix, all device memory:
+ *  a     [n_adapters][max_rank][K] bf16, 16-byte aligned
+ *  b     [n_adapters][N][max_rank] bf16, 16-byte aligned
+ *  rank  [n_adapters] int32 or NULL (= max_rank): the rows of a and columns of
+ *        b in use, taken into [0, max_rank]; what lies past them is not used
+ *        and may hold anything.
+ *  scale [n_adapters] fp32 or NULL (= 1).
+ * max_rank a multiple of 8 in [8, 128]; 1 <= n_adapters <= 4096. */
+typedef struct coli_moe_adapters {
+  int32_t n_adapters;
+  int32_t max_rank;
+  const uint16_t *a;
+  const uint16_t *b;
+  const int32_t *rank;
+  const float *scale;
+} coli_moe_adapters_t;
+
+/* Bytes of workspace of coli_moe_project (backward = 0) or
+ * coli_moe_project_backward (backward != 0); adapters may be NULL, and only
+ * its n_adapters and max_rank are read.  0 for invalid arguments.  Host-only. */
+size_t coli_moe_project_workspace_bytes(const coli_moe_layer_t *layer, int32_t matrix,
+                                        const coli_moe_adapters_t *adapters, int32_t T,
+                                        int32_t backward);
+
+/* y[t] = W x[t] + scale_a * B_a (A_a x[t]),  a the adapter of row t's request:
+ * one weight matrix of one expert slot (expert E is the shared expert) for
+ * every row of the batch, with the requests' adapters beside it.
+ *  matrix 0 = gate, 1 = up (K = H, N = I), 2 = down (K = I, N = H).
+ *  adapters, requests: both given, or both NULL for the projection alone.
+ *  x [T*K] bf16, T in [1, 65536];  y [T*N] bf16 (round-to-nearest-even) or
+ *  fp32 (y_dtype); both 16-byte aligned and not overlapping.
+ * Every row of y is written; rows of no request and requests without an
+ * adapter get the projection alone.  The weights enter exactly (w = q*s),
+ * sums are fp32.  All three weight formats. */
+int coli_moe_project(const coli_moe_layer_t *layer, int32_t expert, int32_t matrix,
+                     const coli_moe_adapters_t *adapters, const coli_moe_requests_t *requests,
+                     const uint16_t *x, int32_t T, void *y, int32_t y_dtype, void *ws,
+                     size_t ws_bytes, void *stream);
+
+/* The backward pass of coli_moe_project for a frozen W, from x and the
+ * gradient dy of y (A x is computed again, nothing is kept from the forward
+ * pass); arguments as there, and
+ *  dy  [T*N] bf16;  with v[t] = scale_a * B_a^T dy[t] and u[t] = scale_a * A_a x[t]:
+ *  dx  [T*K] bf16 or NULL: W^T dy[t] + A_a^T v[t]
+ *  d_a [n_adapters][max_rank][K] fp32: sum over a's rows of v[t] x[t]^T
+ *  d_b [n_adapters][N][max_rank] fp32: sum over a's rows of dy[t] u[t]^T
+ * d_a and d_b are both given or both NULL (and NULL without adapters).  They
+ * are written whole, not added to: zeros for adapters that no row uses and
+ * past an adapter's rank.  At least one output is given.  dx uses W rounded
+ * to bf16. */
+int coli_moe_project_backward(const coli_moe_layer_t *layer, int32_t expert, int32_t matrix,
+                              const coli_moe_adapters_t *adapters,
+                              const coli_moe_requests_t *requests, const uint16_t *x,
+                              const uint16_t *dy, int32_t T, uint16_t *dx, float *d_a,
+                              float *d_b, void *ws, size_t ws_bytes, void *stream);
+
+/* ---- training the router -------------------------------------------------
+ * The batch's T rows hold n_seq sequences; sequence s covers rows
+ * seq_offsets[s] .. seq_offsets[s+1] (ascending, within [0, T]; NULL: one
+ * sequence of all rows, n_seq = 1).  A row counts if it lies in a sequence
+ * and valid[t] is not zero (valid NULL: all).  With n_s counted rows of
+ * sequence s, c_se their choices of expert e, S sequences with n_s > 0, N
+ * counted rows in all, and p_t the row's probabilities -- softmax of its
+ * logits, or for COLI_ROUTE_SIGMOID layers the sigmoids divided by their sum:
+ *   mean_prob[s][e] = (sum over counted t in s of p_te) / n_s
+ *   loss[0] = 1/S sum_s sum_e (E c_se / (k n_s)) mean_prob[s][e]   (balance)
+ *   loss[1] = 1/N sum over counted t of (log sum_e exp logit_te)^2 (z-loss)
+ * Sequences and batches without a counted row give zeros.  Logits of counted
+ * rows are finite or -inf (an expert switched off; a row of -inf alone has
+ * p = 0 and no z term); those of other rows may hold anything.
+ *  seq_offsets [n_seq+1] int32, valid [T] uint8: inputs, device, or NULL.
+ *  counts [n_seq*E] int32, mean_prob [n_seq*E] fp32, tokens [n_seq] int32
+ *  (= n_s), totals [2] int32 (= N, S), loss [2] fp32: device, written by
+ *  coli_moe_balance_loss; coli_moe_route_backward reads counts, tokens and
+ *  totals.  1 <= n_seq <= 65536. */
+typedef struct coli_moe_balance {
+  int32_t n_seq;
+  const int32_t *seq_offsets;
+  const uint8_t *valid;
+  int32_t *counts;
+  float *mean_prob;
+  int32_t *tokens;
+  int32_t *totals;
+  float *loss;
+} coli_moe_balance_t;
+
+/* Bytes of workspace of coli_moe_balance_loss; 0 for invalid arguments. */
+size_t coli_moe_balance_workspace_bytes(const coli_moe_layer_t *layer, int32_t T, int32_t n_seq);
+
+/* Balance loss, z-loss and per-expert counts of a routed batch.  Reads E, k
+ * and the routing function of `layer` (no weights).
+ *  logits [T*E] fp32;  topk_idx [T*k] int32 as coli_moe_route writes it
+ *  (entries outside [0, E) are not counted);  T in [1, 65536], T*k <= 2^20. */
+int coli_moe_balance_loss(const coli_moe_layer_t *layer, const float *logits,
+                          const int32_t *topk_idx, int32_t T, const coli_moe_balance_t *balance,
+                          void *ws, size_t ws_bytes, void *stream);
+
+/* Gradient of the route with respect to the logits, in one pass:
+ *   d_logits = sum_j d_topk_w[t][j] d topk_w[t][j] / d logits
+ *            + d_loss[0] d loss[0] / d logits + d_loss[1] d loss[1] / d logits
+ * where topk_w are the routing weights of coli_moe_route for this layer's
+ * flags and routed_scale, the choice of experts and the counts being
+ * constants.
+ *  d_topk_w [T*k] fp32 or NULL;  balance (the buffers coli_moe_balance_loss
+ *  filled for these logits) and d_loss [2] fp32, device: both given or both
+ *  NULL.  At least one of the two parts is given.
+ *  d_logits [T*E] fp32, every row written; with a balance, rows that do not
+ *  count get zeros (their d_topk_w is not read).  d_logits does not
+ *  overlap the inputs. */
+int coli_moe_route_backward(const coli_moe_layer_t *layer, const float *logits,
+                            const int32_t *topk_idx, int32_t T, const float *d_topk_w,
+                            const coli_moe_balance_t *balance, const float *d_loss,
+                            float *d_logits, void *stream);
+
 /* ---- optional kernel timing ----------------------------------------------
  * For benchmarks and profilers.  After coli_moe_set_trace(t) with t != NULL,
  * every later launch hands t->start[i] and t->stop[i] to the dispatch of its
@@ -418,7 +549,10 @@ enum {
   COLI_K_GEMM_GATEUP = 8, COLI_K_GEMM_DOWN = 9, COLI_K_BLOCK_DOTS = 10,
   COLI_K_ROUTER_LOGITS = 11, COLI_K_QUANTIZE_INT4 = 12, COLI_K_QUANTIZE_INT8 = 13,
   COLI_K_QUANTIZE_MXFP4 = 14, COLI_K_READ_PROBE = 15,
-  COLI_K_MFMA_PROBE = 16, COLI_K_COUNT = 17
+  COLI_K_MFMA_PROBE = 16, COLI_K_BALANCE = 17, COLI_K_BALANCE_FINISH = 18,
+  COLI_K_ROUTE_BACKWARD = 19, COLI_K_PROJECT_PREP = 20, COLI_K_PROJECT_SHRINK = 21,
+  COLI_K_PROJECT_GEMM = 22, COLI_K_PROJECT_FINISH = 23, COLI_K_PROJECT_GRADS = 24,
+  COLI_K_PROJECT_REDUCE = 25, COLI_K_COUNT = 26
 };
 typedef struct coli_moe_trace {
   void **start;     /* hipEvent_t[capacity] */

@@ -45,12 +45,30 @@ class _TraceC(ctypes.Structure):
 KERNEL_NAMES = ["route_fused", "route_topk", "route_group", "decode_gateup", "decode_down",
                 "combine", "quantize_q8_0", "plan", "gemm_gateup", "gemm_down", "block_dots",
                 "router_logits", "quantize_int4", "quantize_int8", "quantize_mxfp4", "read_probe",
-                "mfma_probe"]
+                "mfma_probe", "balance", "balance_finish", "route_backward", "project_prep",
+                "project_shrink", "project_gemm", "project_finish", "project_grads",
+                "project_reduce"]
 
 
 class _RouteC(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "topk_idx", "topk_w", "counts", "offsets", "pairs", "pair_pos", "union_ids", "n_union")]
+
+
+class _AdaptersC(ctypes.Structure):
+    _fields_ = [("n_adapters", ctypes.c_int32), ("max_rank", ctypes.c_int32),
+                ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("rank", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p)]
+
+
+class _RequestsC(ctypes.Structure):
+    _fields_ = [("n_requests", ctypes.c_int32), ("offsets", ctypes.c_void_p),
+                ("adapter", ctypes.c_void_p)]
+
+
+class _BalanceC(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int32)] + [(n, ctypes.c_void_p) for n in (
+        "seq_offsets", "valid", "counts", "mean_prob", "tokens", "totals", "loss")]
 
 
 _lib = None
@@ -87,6 +105,18 @@ def _load():
         lib.coli_moe_block_dots.argtypes = [P(_LayerC), i32, i32, vp, i32, vp, vp]
         lib.coli_moe_quantize_mxfp8.argtypes = [vp, i32, i64, vp, vp, vp]
         lib.coli_moe_mx_dots.argtypes = [P(_LayerC), i32, i32, vp, vp, i32, vp, vp]
+        lib.coli_moe_project_workspace_bytes.argtypes = [P(_LayerC), i32, P(_AdaptersC), i32, i32]
+        lib.coli_moe_project_workspace_bytes.restype = sz
+        lib.coli_moe_project.argtypes = [P(_LayerC), i32, i32, P(_AdaptersC), P(_RequestsC), vp,
+                                         i32, vp, i32, vp, sz, vp]
+        lib.coli_moe_project_backward.argtypes = [P(_LayerC), i32, i32, P(_AdaptersC),
+                                                  P(_RequestsC), vp, vp, i32, vp, vp, vp, vp, sz,
+                                                  vp]
+        lib.coli_moe_balance_workspace_bytes.argtypes = [P(_LayerC), i32, i32]
+        lib.coli_moe_balance_workspace_bytes.restype = sz
+        lib.coli_moe_balance_loss.argtypes = [P(_LayerC), vp, vp, i32, P(_BalanceC), vp, sz, vp]
+        lib.coli_moe_route_backward.argtypes = [P(_LayerC), vp, vp, i32, vp, P(_BalanceC), vp, vp,
+                                                vp]
         lib.coli_moe_strerror.argtypes = [ctypes.c_int]
         lib.coli_moe_strerror.restype = ctypes.c_char_p
         lib.coli_moe_set_trace.argtypes = [ctypes.POINTER(_TraceC)]
@@ -97,7 +127,9 @@ def _load():
                   "coli_moe_forward_decode_noalloc", "coli_moe_forward_prefill", "coli_moe_quantize_q8_0", "coli_moe_block_dots",
                   "coli_moe_quantize_int4_gs64", "coli_moe_quantize_int8_gs64",
                   "coli_moe_quantize_mxfp4", "coli_moe_read_probe",
-                  "coli_moe_mfma_probe", "coli_moe_quantize_mxfp8", "coli_moe_mx_dots"):
+                  "coli_moe_mfma_probe", "coli_moe_quantize_mxfp8", "coli_moe_mx_dots",
+                  "coli_moe_project", "coli_moe_project_backward", "coli_moe_balance_loss",
+                  "coli_moe_route_backward"):
             getattr(lib, f).restype = ctypes.c_int
         _lib = lib
     return _lib
@@ -162,6 +194,66 @@ class Route:
         self.union_ids = torch.empty(E, **i32)
         self.n_union = torch.empty(1, **i32)
         self.c = _RouteC(*[_ptr(getattr(self, n)) for n, _ in _RouteC._fields_])
+
+
+def _need(t, name, dtype, numel, device):
+    """A dense device tensor of this type and at least this many elements, or None."""
+    if t is None:
+        return
+    if (t.dtype != dtype or t.device != device or t.numel() < numel or not t.is_contiguous()):
+        raise ValueError("%s: expected a contiguous %s tensor of at least %d elements on %s, got "
+                         "%s %s on %s%s" % (name, dtype, numel, device, tuple(t.shape), t.dtype,
+                                            t.device, "" if t.is_contiguous() else " (strided)"))
+
+
+class Adapters:
+    """Low-rank adapters of one N x K matrix: a [n, R, K] and b [n, N, R] bf16
+    on the device, R a multiple of 8 up to 128; rank [n] int32 and scale [n]
+    fp32 (both optional) on the device."""
+
+    def __init__(self, a, b, rank=None, scale=None):
+        if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+            raise ValueError("adapters: expected a [n, R, K] and b [n, N, R], got %s and %s"
+                             % (tuple(a.shape), tuple(b.shape)))
+        n, r, k = a.shape
+        _need(a, "a", torch.bfloat16, a.numel(), a.device)
+        _need(b, "b", torch.bfloat16, b.numel(), a.device)
+        _need(rank, "rank", torch.int32, n, a.device)
+        _need(scale, "scale", torch.float32, n, a.device)
+        self.a, self.b, self.rank, self.scale = a, b, rank, scale  # keep the tensors alive
+        self.n, self.r, self.k, self.rows = n, r, k, b.shape[1]
+        self.c = _AdaptersC(n, r, _ptr(a), _ptr(b), _ptr(rank), _ptr(scale))
+
+
+class Requests:
+    """The rows and the adapter of every request of a batch: offsets [n + 1]
+    and adapter [n], int32 on the device (see include/coli_moe.h)."""
+
+    def __init__(self, offsets, adapter):
+        _need(adapter, "adapter", torch.int32, 1, adapter.device)
+        _need(offsets, "offsets", torch.int32, adapter.numel() + 1, adapter.device)
+        self.offsets, self.adapter = offsets, adapter
+        self.c = _RequestsC(adapter.numel(), _ptr(offsets), _ptr(adapter))
+
+
+class Balance:
+    """Sequences and mask of a routed batch, and the device buffers that
+    coli_moe_balance_loss writes: loss [2] (balance, z), counts and mean_prob
+    [n_seq, E], tokens [n_seq], totals [2]."""
+
+    def __init__(self, layer: Layer, n_seq: int = 1, seq_offsets=None, valid=None, device="cuda"):
+        device = torch.device(device) if seq_offsets is None else seq_offsets.device
+        E = layer.n_experts
+        self.seq_offsets, self.valid = seq_offsets, valid
+        self.counts = torch.empty(n_seq, E, dtype=torch.int32, device=device)
+        self.mean_prob = torch.empty(n_seq, E, dtype=torch.float32, device=device)
+        self.tokens = torch.empty(n_seq, dtype=torch.int32, device=device)
+        self.totals = torch.empty(2, dtype=torch.int32, device=device)
+        self.loss = torch.empty(2, dtype=torch.float32, device=device)
+        device = self.loss.device
+        _need(seq_offsets, "seq_offsets", torch.int32, n_seq + 1, device)
+        _need(valid, "valid", torch.uint8, 1, device)
+        self.c = _BalanceC(n_seq, *[_ptr(getattr(self, n)) for n, _ in _BalanceC._fields_[1:]])
 
 
 def coli_moe_strerror(status: int) -> str:
@@ -278,6 +370,120 @@ def coli_moe_mx_dots(layer: Layer, expert: int, matrix: int, q_act, e_act, T: in
     _check("coli_moe_mx_dots", _load().coli_moe_mx_dots(
         ctypes.byref(layer.c), expert, matrix, _ptr(q_act), _ptr(e_act), T, _ptr(out),
         _stream(stream)))
+
+
+def _shape_nk(layer: Layer, matrix: int):
+    return (layer.hidden, layer.inter) if matrix == 2 else (layer.inter, layer.hidden)
+
+
+def _run(name, on, stream, *args):
+    """Calls the library on the device of tensor `on`: by default on that
+    device's current stream, which is made current for the call if it is not."""
+    fn = getattr(_load(), name)
+    if not on.is_cuda:
+        raise ValueError("%s: tensors have to be on the GPU, got %s" % (name, on.device))
+    s = torch.cuda.current_stream(on.device).cuda_stream if stream is None else _stream(stream)
+    if on.device.index == torch.cuda.current_device():
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(on.device):
+            rc = fn(*args, s)
+    _check(name, rc)
+
+
+def _ws(ws, on):
+    """Pointer and bytes of a workspace."""
+    _need(ws, "ws", ws.dtype, 0, on.device)
+    return _ptr(ws), ws.numel() * ws.element_size()
+
+
+def coli_moe_project_workspace_bytes(layer: Layer, matrix: int, adapters, T: int,
+                                     backward: bool = False) -> int:
+    return int(_load().coli_moe_project_workspace_bytes(
+        ctypes.byref(layer.c), matrix, None if adapters is None else ctypes.byref(adapters.c), T,
+        int(backward)))
+
+
+def project_workspace(layer: Layer, matrix: int, adapters, T: int, backward: bool = False,
+                      device="cuda") -> torch.Tensor:
+    """A device buffer large enough for coli_moe_project[_backward] at T rows."""
+    n = coli_moe_project_workspace_bytes(layer, matrix, adapters, T, backward)
+    return torch.empty(max(n, 256), dtype=torch.uint8,
+                       device=device if adapters is None else adapters.a.device)
+
+
+def _project_args(layer, matrix, adapters, requests, x, T):
+    n, k = _shape_nk(layer, matrix)
+    _need(x, "x", torch.bfloat16, T * k, x.device)
+    if adapters is not None and (adapters.k != k or adapters.rows != n):
+        raise ValueError("adapters of a %d x %d matrix given for a %d x %d one"
+                         % (adapters.rows, adapters.k, n, k))
+    for t, name in ((adapters and adapters.a, "adapters"), (requests and requests.adapter, "requests")):
+        if t is not None and t.device != x.device:
+            raise ValueError("%s on %s, x on %s" % (name, t.device, x.device))
+    return n, k, (None if adapters is None else ctypes.byref(adapters.c),
+                  None if requests is None else ctypes.byref(requests.c))
+
+
+def coli_moe_project(layer: Layer, expert: int, matrix: int, adapters, requests, x, T: int, y,
+                     y_dtype: int, ws, stream=None):
+    """y = x W^T + the requests' adapters (adapters and requests may both be None)."""
+    n, _, (ad, rq) = _project_args(layer, matrix, adapters, requests, x, T)
+    _need(y, "y", torch.float32 if y_dtype == COLI_OUT_F32 else torch.bfloat16, T * n, x.device)
+    _run("coli_moe_project", x, stream, ctypes.byref(layer.c), expert, matrix, ad, rq, _ptr(x), T,
+         _ptr(y), y_dtype, *_ws(ws, x))
+
+
+def coli_moe_project_backward(layer: Layer, expert: int, matrix: int, adapters, requests, x, dy,
+                              T: int, dx, d_a, d_b, ws, stream=None):
+    """dx (bf16), d_a and d_b (fp32) of coli_moe_project; dx, or d_a and d_b, may be None."""
+    n, k, (ad, rq) = _project_args(layer, matrix, adapters, requests, x, T)
+    _need(dy, "dy", torch.bfloat16, T * n, x.device)
+    _need(dx, "dx", torch.bfloat16, T * k, x.device)
+    if adapters is not None:
+        _need(d_a, "d_a", torch.float32, adapters.a.numel(), x.device)
+        _need(d_b, "d_b", torch.float32, adapters.b.numel(), x.device)
+    _run("coli_moe_project_backward", x, stream, ctypes.byref(layer.c), expert, matrix, ad, rq,
+         _ptr(x), _ptr(dy), T, _ptr(dx), _ptr(d_a), _ptr(d_b), *_ws(ws, x))
+
+
+def coli_moe_balance_workspace_bytes(layer: Layer, T: int, n_seq: int = 1) -> int:
+    return int(_load().coli_moe_balance_workspace_bytes(ctypes.byref(layer.c), T, n_seq))
+
+
+def balance_workspace(layer: Layer, T: int, n_seq: int = 1, device="cuda") -> torch.Tensor:
+    """A device buffer large enough for coli_moe_balance_loss at T tokens."""
+    return torch.empty(max(coli_moe_balance_workspace_bytes(layer, T, n_seq), 256),
+                       dtype=torch.uint8, device=device)
+
+
+def _balance_args(layer, logits, topk_idx, T, balance):
+    _need(logits, "logits", torch.float32, T * layer.n_experts, logits.device)
+    _need(topk_idx, "topk_idx", torch.int32, T * layer.top_k, logits.device)
+    if balance is not None:
+        _need(balance.valid, "valid", torch.uint8, T, logits.device)
+        _need(balance.counts, "balance", torch.int32, balance.c.n_seq * layer.n_experts,
+              logits.device)
+
+
+def coli_moe_balance_loss(layer: Layer, logits, topk_idx, T: int, balance: Balance, ws,
+                          stream=None):
+    _balance_args(layer, logits, topk_idx, T, balance)
+    _run("coli_moe_balance_loss", logits, stream, ctypes.byref(layer.c), _ptr(logits),
+         _ptr(topk_idx), T, ctypes.byref(balance.c), *_ws(ws, logits))
+
+
+def coli_moe_route_backward(layer: Layer, logits, topk_idx, T: int, d_topk_w, balance, d_loss,
+                            d_logits, stream=None):
+    """d_logits of the routing weights (d_topk_w) and of the balance and z-losses
+    (balance, d_loss); either part may be None."""
+    _balance_args(layer, logits, topk_idx, T, balance)
+    _need(d_topk_w, "d_topk_w", torch.float32, T * layer.top_k, logits.device)
+    _need(d_loss, "d_loss", torch.float32, 2, logits.device)
+    _need(d_logits, "d_logits", torch.float32, T * layer.n_experts, logits.device)
+    _run("coli_moe_route_backward", logits, stream, ctypes.byref(layer.c), _ptr(logits),
+         _ptr(topk_idx), T, _ptr(d_topk_w), None if balance is None else ctypes.byref(balance.c),
+         _ptr(d_loss), _ptr(d_logits))
 
 
 def _hip_runtime():

@@ -101,6 +101,49 @@ int check_forward(const coli_moe_layer_t *layer, const coli_moe_route_t *route,
   return check_ws(ws, ws_bytes, need);
 }
 
+constexpr int kMaxSpans = 65536;  // requests or sequences of a batch
+constexpr int kMaxAdapters = 4096;
+constexpr int kMaxRank = 128;
+
+int check_adapter_sizes(const coli_moe_adapters_t *a) {
+  if (a->n_adapters < 1 || a->n_adapters > kMaxAdapters) return COLI_E_INVALID;
+  if (a->max_rank < 8 || a->max_rank > kMaxRank || a->max_rank % 8) return COLI_E_INVALID;
+  return COLI_OK;
+}
+
+// What coli_moe_project and its backward pass have in common.
+int check_project(const coli_moe_layer_t *layer, int expert, int matrix,
+                  const coli_moe_adapters_t *a, const coli_moe_requests_t *r, const uint16_t *x,
+                  int T, Layer *L) {
+  int rc = check_layer(layer, L);
+  if (rc) return rc;
+  if ((rc = check_weights(*L))) return rc;
+  if (expert < 0 || expert >= L->E + L->S || matrix < 0 || matrix > 2) return COLI_E_INVALID;
+  if (T < 1 || T > kMaxT || !x) return COLI_E_INVALID;
+  if (!a != !r) return COLI_E_INVALID;
+  if (a) {
+    if ((rc = check_adapter_sizes(a))) return rc;
+    if (!a->a || !a->b || !r->offsets || !r->adapter) return COLI_E_INVALID;
+    if (r->n_requests < 1 || r->n_requests > kMaxSpans) return COLI_E_INVALID;
+    if (!aligned(a->a, 16) || !aligned(a->b, 16) || !aligned(a->rank, 4) ||
+        !aligned(a->scale, 4) || !aligned(r->offsets, 4) || !aligned(r->adapter, 4))
+      return COLI_E_ALIGN;
+  }
+  return aligned(x, 16) ? COLI_OK : COLI_E_ALIGN;
+}
+
+// Layer, sizes and inputs of the router's training calls.
+int check_balance(const Layer &L, const coli_moe_balance_t *b, bool outputs) {
+  if (!b || b->n_seq < 1 || b->n_seq > kMaxSpans) return COLI_E_INVALID;
+  if (!b->seq_offsets && b->n_seq != 1) return COLI_E_INVALID;
+  if (!b->counts || !b->tokens || !b->totals) return COLI_E_INVALID;
+  if (outputs && (!b->mean_prob || !b->loss)) return COLI_E_INVALID;
+  if (!aligned(b->seq_offsets, 4) || !aligned(b->counts, 4) || !aligned(b->tokens, 4) ||
+      !aligned(b->totals, 4) || !aligned(b->mean_prob, 4) || !aligned(b->loss, 4))
+    return COLI_E_ALIGN;
+  return COLI_OK;
+}
+
 }  // namespace
 }  // namespace coli
 
@@ -323,6 +366,92 @@ int coli_moe_mx_dots(const coli_moe_layer_t *layer, int32_t expert, int32_t matr
   if (!aligned(q_act, 16) || !aligned(e_act, 4) || !aligned(out, 16)) return COLI_E_ALIGN;
   return launch_mx_dots(L, expert, matrix, q_act, e_act, T, out,
                         reinterpret_cast<hipStream_t>(stream));
+}
+
+size_t coli_moe_project_workspace_bytes(const coli_moe_layer_t *layer, int32_t matrix,
+                                        const coli_moe_adapters_t *adapters, int32_t T,
+                                        int32_t backward) {
+  Layer L;
+  if (check_layer(layer, &L) || matrix < 0 || matrix > 2 || T < 1 || T > kMaxT) return 0;
+  if (adapters && check_adapter_sizes(adapters)) return 0;
+  return project_workspace(L, matrix, adapters ? adapters->n_adapters : 0,
+                           adapters ? adapters->max_rank : 0, T, backward);
+}
+
+int coli_moe_project(const coli_moe_layer_t *layer, int32_t expert, int32_t matrix,
+                     const coli_moe_adapters_t *adapters, const coli_moe_requests_t *requests,
+                     const uint16_t *x, int32_t T, void *y, int32_t y_dtype, void *ws,
+                     size_t ws_bytes, void *stream) {
+  Layer L;
+  int rc = check_project(layer, expert, matrix, adapters, requests, x, T, &L);
+  if (rc) return rc;
+  if (!y || (y_dtype != COLI_OUT_BF16 && y_dtype != COLI_OUT_F32)) return COLI_E_INVALID;
+  if (!aligned(y, 16)) return COLI_E_ALIGN;
+  if ((rc = check_ws(ws, ws_bytes,
+                     project_workspace(L, matrix, adapters ? adapters->n_adapters : 0,
+                                       adapters ? adapters->max_rank : 0, T, 0))))
+    return rc;
+  return launch_project(L, expert, matrix, adapters, requests, x, T, y, y_dtype, ws,
+                        reinterpret_cast<hipStream_t>(stream));
+}
+
+int coli_moe_project_backward(const coli_moe_layer_t *layer, int32_t expert, int32_t matrix,
+                              const coli_moe_adapters_t *adapters,
+                              const coli_moe_requests_t *requests, const uint16_t *x,
+                              const uint16_t *dy, int32_t T, uint16_t *dx, float *d_a,
+                              float *d_b, void *ws, size_t ws_bytes, void *stream) {
+  Layer L;
+  int rc = check_project(layer, expert, matrix, adapters, requests, x, T, &L);
+  if (rc) return rc;
+  if (!dy || !d_a != !d_b || (d_a && !adapters) || (!dx && !d_a)) return COLI_E_INVALID;
+  if (!aligned(dy, 16) || !aligned(dx, 16) || !aligned(d_a, 16) || !aligned(d_b, 16))
+    return COLI_E_ALIGN;
+  if ((rc = check_ws(ws, ws_bytes,
+                     project_workspace(L, matrix, adapters ? adapters->n_adapters : 0,
+                                       adapters ? adapters->max_rank : 0, T, 1))))
+    return rc;
+  return launch_project_backward(L, expert, matrix, adapters, requests, x, dy, T, dx, d_a, d_b,
+                                 ws, reinterpret_cast<hipStream_t>(stream));
+}
+
+size_t coli_moe_balance_workspace_bytes(const coli_moe_layer_t *layer, int32_t T, int32_t n_seq) {
+  Layer L;
+  if (check_layer(layer, &L) || check_tokens(L, T, kMaxT) || n_seq < 1 || n_seq > kMaxSpans)
+    return 0;
+  return balance_workspace(L, T);
+}
+
+int coli_moe_balance_loss(const coli_moe_layer_t *layer, const float *logits,
+                          const int32_t *topk_idx, int32_t T, const coli_moe_balance_t *balance,
+                          void *ws, size_t ws_bytes, void *stream) {
+  Layer L;
+  int rc = check_layer(layer, &L);
+  if (rc) return rc;
+  if ((rc = check_tokens(L, T, kMaxT))) return rc;
+  if (!logits || !topk_idx) return COLI_E_INVALID;
+  if ((rc = check_balance(L, balance, true))) return rc;
+  if (!aligned(logits, 4) || !aligned(topk_idx, 4)) return COLI_E_ALIGN;
+  if ((rc = check_ws(ws, ws_bytes, balance_workspace(L, T)))) return rc;
+  return launch_balance(L, logits, topk_idx, T, *balance, ws,
+                        reinterpret_cast<hipStream_t>(stream));
+}
+
+int coli_moe_route_backward(const coli_moe_layer_t *layer, const float *logits,
+                            const int32_t *topk_idx, int32_t T, const float *d_topk_w,
+                            const coli_moe_balance_t *balance, const float *d_loss,
+                            float *d_logits, void *stream) {
+  Layer L;
+  int rc = check_layer(layer, &L);
+  if (rc) return rc;
+  if ((rc = check_tokens(L, T, kMaxT))) return rc;
+  if (!logits || !topk_idx || !d_logits || !balance != !d_loss || (!d_topk_w && !balance))
+    return COLI_E_INVALID;
+  if (balance && (rc = check_balance(L, balance, false))) return rc;
+  if (!aligned(logits, 4) || !aligned(topk_idx, 4) || !aligned(d_topk_w, 4) ||
+      !aligned(d_loss, 4) || !aligned(d_logits, 4))
+    return COLI_E_ALIGN;
+  return launch_route_backward(L, logits, topk_idx, T, d_topk_w, balance, d_loss, d_logits,
+                               reinterpret_cast<hipStream_t>(stream));
 }
 
 int coli_moe_set_trace(coli_moe_trace_t *trace) {

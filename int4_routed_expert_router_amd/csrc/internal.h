@@ -71,6 +71,24 @@ int launch_quantize_mxfp8(const void *src, int src_dtype, int64_t n, uint8_t *q,
 int launch_mx_dots(const Layer &L, int expert, int matrix, const uint8_t *qa, const uint8_t *ea,
                    int T, float *out, hipStream_t s);
 
+// Projection with adapters and its backward pass (project.hip); ad and rq are
+// both given or both NULL.
+size_t project_workspace(const Layer &L, int matrix, int n_adapters, int max_rank, int T,
+                         int backward);
+int launch_project(const Layer &L, int expert, int matrix, const coli_moe_adapters_t *ad,
+                   const coli_moe_requests_t *rq, const uint16_t *x, int T, void *y, int y_dtype,
+                   void *ws, hipStream_t s);
+int launch_project_backward(const Layer &L, int expert, int matrix, const coli_moe_adapters_t *ad,
+                            const coli_moe_requests_t *rq, const uint16_t *x, const uint16_t *dy,
+                            int T, uint16_t *dx, float *d_a, float *d_b, void *ws, hipStream_t s);
+// Balance loss and the route's gradient (balance.hip).
+size_t balance_workspace(const Layer &L, int T);
+int launch_balance(const Layer &L, const float *logits, const int32_t *idx, int T,
+                   const coli_moe_balance_t &b, void *ws, hipStream_t s);
+int launch_route_backward(const Layer &L, const float *logits, const int32_t *idx, int T,
+                          const float *d_w, const coli_moe_balance_t *b, const float *d_loss,
+                          float *d_logits, hipStream_t s);
+
 inline int hip_status(hipError_t e) { return e == hipSuccess ? COLI_OK : COLI_E_HIP; }
 
 // Optional per-kernel timing (coli_moe_set_trace).  Every kernel goes out
