@@ -552,7 +552,8 @@ enum {
   COLI_K_MFMA_PROBE = 16, COLI_K_BALANCE = 17, COLI_K_BALANCE_FINISH = 18,
   COLI_K_ROUTE_BACKWARD = 19, COLI_K_PROJECT_PREP = 20, COLI_K_PROJECT_SHRINK = 21,
   COLI_K_PROJECT_GEMM = 22, COLI_K_PROJECT_FINISH = 23, COLI_K_PROJECT_GRADS = 24,
-  COLI_K_PROJECT_REDUCE = 25, COLI_K_COUNT = 26
+  COLI_K_PROJECT_REDUCE = 25, COLI_K_PROJECT_STREAM = 26, COLI_K_PROJECT_COMBINE = 27,
+  COLI_K_COUNT = 28
 };
 typedef struct coli_moe_trace {
   void **start;     /* hipEvent_t[capacity] */

@@ -47,7 +47,7 @@ KERNEL_NAMES = ["route_fused", "route_topk", "route_group", "decode_gateup", "de
                 "router_logits", "quantize_int4", "quantize_int8", "quantize_mxfp4", "read_probe",
                 "mfma_probe", "balance", "balance_finish", "route_backward", "project_prep",
                 "project_shrink", "project_gemm", "project_finish", "project_grads",
-                "project_reduce"]
+                "project_reduce", "project_stream", "project_combine"]
 
 
 class _RouteC(ctypes.Structure):

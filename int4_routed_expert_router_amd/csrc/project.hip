@@ -83,6 +83,25 @@ COLI_DEV uint4 keep_first(uint4 v, int n) {
   return make_uint4(d[0], d[1], d[2], d[3]);
 }
 
+// Sum of A accumulators over NW wavefronts, in wavefront 0, pairwise through
+// LDS (buf: NW/2 * A rows).
+template <int A, int NW>
+COLI_DEV void wave_sums(f32x4 *acc, f32x4 (*buf)[64], int wv, int lane) {
+#pragma unroll
+  for (int half = NW / 2; half > 0; half >>= 1) {
+    __syncthreads();
+    if (wv >= half && wv < 2 * half) {
+#pragma unroll
+      for (int i = 0; i < A; ++i) buf[(wv - half) * A + i][lane] = acc[i];
+    }
+    __syncthreads();
+    if (wv < half) {
+#pragma unroll
+      for (int i = 0; i < A; ++i) acc[i] += buf[wv * A + i][lane];
+    }
+  }
+}
+
 struct Adapters {
   const uint16_t *a, *b;  // [n][R][K], [n][N][R]
   const int32_t *rank;    // [n] or NULL
@@ -264,28 +283,28 @@ struct ShrinkArgs {
   int T, F, R, R32, splits, nsub;
 };
 
-// One workgroup per 64-row tile, split and residue of the tile's requests
-// modulo nsub (so that a tile of many one-row requests spreads over many
-// workgroups).  Its four wavefronts take the split's 64-wide k blocks in
+// One workgroup per tile of 16 MI rows, split and residue of the tile's
+// requests modulo nsub (so that a tile of many one-row requests spreads over
+// many workgroups).  Its NW wavefronts take the split's 64-wide k blocks in
 // turn; operands come straight from memory: lane (c, g) holds 16 values of
 // row c at k = 16g, two matrix-core steps.
-template <int RT>
+template <int RT, int MI, int NW>
 COLI_DEV void shrink_tile(const ShrinkArgs &g, int tile, int sub, int split, f32x4 (*buf)[64]) {
   const int lane = threadIdx.x & 63, c = lane & 15, kg = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int t0 = tile * 64, t1 = min(g.T, t0 + 64);
+  const int t0 = tile * (16 * MI), t1 = min(g.T, t0 + 16 * MI);
   const int nb = g.F / 64;
   for_requests(g.q, t0, t1, [&](int ordinal, int begin, int end, int a) {
     if (ordinal % g.nsub != sub) return;
     const int rank = rank_of(g.rank, a, g.R);
-    f32x4 acc[4][RT];
+    f32x4 acc[MI][RT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int r = 0; r < RT; ++r) acc[i][r] = f32x4{0, 0, 0, 0};
     const uint16_t *mrow = g.m + ((int64_t)a * g.R + c) * g.F + 16 * kg;
     const uint16_t *zrow = g.z + (int64_t)(t0 + c) * g.F + 16 * kg;
-    for (int b = split * 4 + wv; b < nb; b += 4 * g.splits) {
+    for (int b = split * NW + wv; b < nb; b += NW * g.splits) {
       uint4 mf[RT][2];
 #pragma unroll
       for (int r = 0; r < RT; ++r)
@@ -293,8 +312,8 @@ COLI_DEV void shrink_tile(const ShrinkArgs &g, int tile, int sub, int split, f32
         for (int h = 0; h < 2; ++h)
           mf[r][h] = 16 * r + c < rank ? ld16(mrow + (int64_t)16 * r * g.F + 64 * b + 8 * h) : zero4();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (begin >= t0 + 16 * i + 16 || end <= t0 + 16 * i) continue;
+      for (int i = 0; i < MI; ++i) {
+        if (MI > 1 && (begin >= t0 + 16 * i + 16 || end <= t0 + 16 * i)) continue;
         const int t = t0 + 16 * i + c;
         uint4 zf[2];
 #pragma unroll
@@ -306,28 +325,11 @@ COLI_DEV void shrink_tile(const ShrinkArgs &g, int tile, int sub, int split, f32
           for (int r = 0; r < RT; ++r) acc[i][r] = mfma(zf[h], mf[r][h], acc[i][r]);
       }
     }
-    // the four wavefronts' sums, pairwise
-#pragma unroll
-    for (int half = 2; half > 0; half >>= 1) {
-      __syncthreads();
-      if (wv >= half && wv < 2 * half) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int r = 0; r < RT; ++r) buf[((wv - half) * 4 + i) * RT + r][lane] = acc[i][r];
-      }
-      __syncthreads();
-      if (wv < half) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int r = 0; r < RT; ++r) acc[i][r] += buf[(wv * 4 + i) * RT + r][lane];
-      }
-    }
+    wave_sums<MI * RT, NW>(&acc[0][0], buf, wv, lane);
     if (wv == 0) {
       const float s = g.scale ? g.scale[a] : 1.0f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -346,30 +348,59 @@ __global__ void __launch_bounds__(256) shrink_kernel(ShrinkArgs g0, ShrinkArgs g
   // z: the first operand's splits, then the second's
   const bool second = (int)blockIdx.z >= g0.splits;
   const ShrinkArgs &g = second ? g1 : g0;
-  shrink_tile<RT>(g, blockIdx.x, blockIdx.y, second ? blockIdx.z - g0.splits : blockIdx.z, buf);
+  shrink_tile<RT, 4, 4>(g, blockIdx.x, blockIdx.y, second ? blockIdx.z - g0.splits : blockIdx.z, buf);
 }
 
 // ------------------------------------------------------------------- gemm
 
-struct GemmArgs {
-  const uint16_t *x;  // [T][K] bf16
-  const uint16_t *w;  // [N][K] bf16
-  const float *sc;    // [K/64][N] or unused
-  int T, N, K;
-  void *y;  // [T][N]
-  // adapters: u [splits][T][R32] fp32, b [n][N][R] bf16
+// The adapters' side of an output: b [n][N][R] bf16 and shrink's u.
+struct ExpandArgs {
   Requests q;
-  const float *u;
+  const float *u;  // [splits][T][R32]
   const uint16_t *b;
   const int32_t *rank;
-  int R, R32, splits;
+  int T, N, R, R32, splits;
 };
+
+// This lane's operand values u[t][k .. k+8), the splits added up, as P parts.
+template <int P>
+COLI_DEV void load_u(const ExpandArgs &g, int t, int k, bool live, uint4 (&uf)[P]) {
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+  if (live) {
+    const float *p = g.u + (int64_t)t * g.R32 + k;
+#pragma unroll 4
+    for (int s = 0; s < g.splits; ++s) {
+      const float4 lo = *reinterpret_cast<const float4 *>(p + (int64_t)s * g.T * g.R32);
+      const float4 hi = *reinterpret_cast<const float4 *>(p + (int64_t)s * g.T * g.R32 + 4);
+      v[0] += lo.x;
+      v[1] += lo.y;
+      v[2] += lo.z;
+      v[3] += lo.w;
+      v[4] += hi.x;
+      v[5] += hi.y;
+      v[6] += hi.z;
+      v[7] += hi.w;
+    }
+  }
+  split8<P>(v, uf);
+}
+// Ranks [k, k + 8) of the adapter's columns n0 + 4c + j.
+COLI_DEV void load_b(const ExpandArgs &g, int a, int n0, int k, int rank, uint4 (&bf)[4]) {
+  const int c = threadIdx.x & 15;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int n = min(n0 + 4 * c + j, g.N - 1);
+    bf[j] = k < rank ? keep_first(ld16(g.b + ((int64_t)a * g.N + n) * g.R + k), rank - k) : zero4();
+  }
+}
 
 // acc += the adapters' part of the wavefront's MI x 4 tiles: rows t0 + 16i +
 // c, columns n0 + 4c + j.  Every request with rows here multiplies only the
 // 16-row tiles that it reaches, its other rows as zeros.
 template <int MI, int P>
-COLI_DEV void expand(const GemmArgs &g, int t0, int n0, f32x4 (&acc)[MI][4]) {
+COLI_DEV void expand(const ExpandArgs &g, int t0, int n0, f32x4 (&acc)[MI][4]) {
   const int lane = threadIdx.x & 63, c = lane & 15, kg = lane >> 4;
   const int t1 = min(g.T, t0 + 16 * MI);
   if (t0 >= t1) return;
@@ -378,34 +409,13 @@ COLI_DEV void expand(const GemmArgs &g, int t0, int n0, f32x4 (&acc)[MI][4]) {
     for (int k0 = 0; k0 < rank; k0 += 32) {
       const int k = k0 + 8 * kg;  // this lane's eight ranks
       uint4 bf[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = min(n0 + 4 * c + j, g.N - 1);
-        bf[j] = k < rank ? keep_first(ld16(g.b + ((int64_t)a * g.N + n) * g.R + k), rank - k) : zero4();
-      }
+      load_b(g, a, n0, k, rank, bf);
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
         if (begin >= t0 + 16 * i + 16 || end <= t0 + 16 * i) continue;
         const int t = t0 + 16 * i + c;
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-        if (t >= begin && t < end && k < rank) {
-          for (int s = 0; s < g.splits; ++s) {
-            const float4 *p = reinterpret_cast<const float4 *>(g.u + ((int64_t)s * g.T + t) * g.R32 + k);
-            const float4 lo = p[0], hi = p[1];
-            v[0] += lo.x;
-            v[1] += lo.y;
-            v[2] += lo.z;
-            v[3] += lo.w;
-            v[4] += hi.x;
-            v[5] += hi.y;
-            v[6] += hi.z;
-            v[7] += hi.w;
-          }
-        }
         uint4 uf[P];
-        split8<P>(v, uf);
+        load_u<P>(g, t, k, t >= begin && t < end && k < rank, uf);
 #pragma unroll
         for (int p = 0; p < P; ++p)
 #pragma unroll
@@ -414,6 +424,25 @@ COLI_DEV void expand(const GemmArgs &g, int t0, int n0, f32x4 (&acc)[MI][4]) {
     }
   });
 }
+
+// Four neighbouring columns of one row.
+template <bool F32>
+COLI_DEV void store4(void *y, int64_t at, float a, float b, float c, float d) {
+  if (F32)
+    *reinterpret_cast<float4 *>(static_cast<float *>(y) + at) = make_float4(a, b, c, d);
+  else
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(y) + at) =
+        make_uint2(pack_bf16(a, b), pack_bf16(c, d));
+}
+
+struct GemmArgs {
+  const uint16_t *x;  // [T][K] bf16
+  const uint16_t *w;  // [N][K] bf16
+  const float *sc;    // [K/64][N] or unused
+  int T, N, K;
+  void *y;  // [T][N]
+  ExpandArgs e;  // u NULL: no adapters
+};
 
 // BM x BN tile, wavefronts of WM x 64.  Stages of 64 k go global -> LDS by
 // DMA, two in turn.  A row's 16-byte chunk q is kept at q ^ (row & 7) for x
@@ -489,21 +518,273 @@ __global__ void __launch_bounds__(BM / WM *BN / 64 * 64) gemm_kernel(GemmArgs g)
     }
   }
   if (!cols) return;
-  if (g.u) expand<MI, F32 ? 3 : 2>(g, tm + wm, n0, acc);
+  if (g.e.u) expand<MI, F32 ? 3 : 2>(g.e, tm + wm, n0, acc);
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int t = tm + wm + 16 * i + 4 * kg + e;
-      if (t >= g.T) continue;
-      const int64_t at = (int64_t)t * g.N + n0 + 4 * c;
-      if (F32)
-        *reinterpret_cast<float4 *>(static_cast<float *>(g.y) + at) =
-            make_float4(acc[i][0][e], acc[i][1][e], acc[i][2][e], acc[i][3][e]);
-      else
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(g.y) + at) = make_uint2(
-            pack_bf16(acc[i][0][e], acc[i][1][e]), pack_bf16(acc[i][2][e], acc[i][3][e]));
+      if (t < g.T)
+        store4<F32>(g.y, (int64_t)t * g.N + n0 + 4 * c, acc[i][0][e], acc[i][1][e], acc[i][2][e],
+                    acc[i][3][e]);
     }
+}
+
+// ----------------------------------------------------------------- stream
+//
+// Short batches: the codes go from memory straight into registers, so that a
+// call costs one pass over the container and two launches.  The first
+// computes W x in parts (split along K) and u side by side; the second adds
+// the parts and the adapters.
+
+struct StreamArgs {
+  Matrix m;
+  const uint16_t *x;  // [T][K]
+  float *part;        // [splits][T][N]
+  int T, splits, per;  // per: 64-wide groups of a wavefront
+  int shrink_blocks, shrink_tiles;
+  ShrinkArgs s;
+};
+
+constexpr int kStreamWaves = 8;
+
+// Raw operands of one 64-wide group of a row: 16 codes per lane (k = 16g of
+// the group, g = lane / 16), in two steps of eight.
+template <int F>
+struct Raw {
+  uint32_t w[F == kI8 ? 4 : 2];
+  uint32_t s;
+};
+template <int F>
+COLI_DEV Raw<F> load_raw(const Matrix &m, int n, int b, int kg) {
+  Raw<F> r;
+  if (F == kI8) {
+    const uint4 v = ld16(m.q + (int64_t)n * m.K + 64 * b + 16 * kg);
+    r.w[F == kI8 ? 2 : 0] = v.z;
+    r.w[F == kI8 ? 3 : 0] = v.w;
+    r.w[0] = v.x;
+    r.w[1] = v.y;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2 *>(m.q + ((int64_t)n * m.K + 64 * b + 16 * kg) / 2);
+    r.w[0] = v.x;
+    r.w[1] = v.y;
+  }
+  if (F == kF4) r.s = m.sc[(int64_t)n * (m.K / 32) + 2 * b + (kg >> 1)];
+  else r.s = reinterpret_cast<const uint16_t *>(m.sc)[(int64_t)n * (m.K / 64) + b];
+  return r;
+}
+// Step h as a matrix-core operand.  int4: the bf16 value 24 + q (a nibble in
+// the mantissa of 16 .. 31), pairs (k, k + 4); the bias leaves through the
+// accumulator's start value, -24 times the row's sum of x.  int8: exact
+// values.  MXFP4: the weights themselves.
+template <int F>
+COLI_DEV uint4 unpack(const Raw<F> &r, int h) {
+  if (F == kI4) {
+    const uint32_t w = r.w[h];
+    constexpr uint32_t M = 0x00780078u, X = 0x41c041c0u;
+    return make_uint4(__builtin_amdgcn_bitop3_b32(w << 3, M, X, kAndXor),
+                      __builtin_amdgcn_bitop3_b32(w >> 1, M, X, kAndXor),
+                      __builtin_amdgcn_bitop3_b32(w >> 5, M, X, kAndXor),
+                      __builtin_amdgcn_bitop3_b32(w >> 9, M, X, kAndXor));
+  }
+  if (F == kI8) {
+    uint32_t d[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t v = r.w[F == kI8 ? 2 * h + i : 0];
+      d[2 * i] = pack_bf16((float)(int8_t)v, (float)(int8_t)(v >> 8));
+      d[2 * i + 1] = pack_bf16((float)(int8_t)(v >> 16), (float)(int8_t)(v >> 24));
+    }
+    return make_uint4(d[0], d[1], d[2], d[3]);
+  }
+  const float s = __uint_as_float(r.s ? r.s << 23 : 0x00400000u);
+  const uint32_t w = r.w[h];
+  return make_uint4(
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0)),
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1)),
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2)),
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3)));
+}
+
+// One workgroup: 16 MT rows x 16 NJ columns (n0 + NJ c + j) over one split of
+// K; its wavefronts take neighbouring runs of `per` groups, GB of them loaded
+// ahead of their use.
+template <int F, int MT, int NJ, int GB>
+COLI_DEV void stream_tile(const StreamArgs &g, int nt, int tt, int split, f32x4 (*buf)[64]) {
+  const int lane = threadIdx.x & 63, c = lane & 15, kg = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = nt * (16 * NJ), t0 = tt * (16 * MT);
+  const int b0 = (split * kStreamWaves + wv) * g.per, b1 = min(g.m.K / 64, b0 + g.per);
+  f32x4 acc[MT][NJ];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  const uint16_t *xrow = g.x + (int64_t)(t0 + c) * g.m.K + 16 * kg;
+  for (int b = b0; b < b1; b += GB) {
+    Raw<F> raw[GB][NJ];
+    uint4 xr[GB][MT][2];
+#pragma unroll
+    for (int i = 0; i < GB; ++i) {
+      if (b + i >= b1) continue;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) raw[i][j] = load_raw<F>(g.m, n0 + NJ * c + j, b + i, kg);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          xr[i][m][h] = t0 + 16 * m + c < g.T
+                            ? ld16(xrow + (int64_t)16 * m * g.m.K + 64 * (b + i) + 8 * h)
+                            : zero4();
+    }
+#pragma unroll
+    for (int i = 0; i < GB; ++i) {
+      if (b + i >= b1) continue;
+      f32x4 start[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        start[m] = f32x4{0, 0, 0, 0};
+        if (F == kI4) {
+          constexpr uint32_t kMinus24 = 0xc1c0c1c0u;
+          const uint4 ones = make_uint4(kMinus24, kMinus24, kMinus24, kMinus24);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t d[4] = {xr[i][m][h].x, xr[i][m][h].y, xr[i][m][h].z, xr[i][m][h].w};
+            uint32_t o[4];
+            x8_to_pairs(d, o);
+            xr[i][m][h] = make_uint4(o[0], o[1], o[2], o[3]);
+            start[m] = mfma(xr[i][m][h], ones, start[m]);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const uint4 w0 = unpack<F>(raw[i][j], 0), w1 = unpack<F>(raw[i][j], 1);
+        const float s = F == kF4 ? 1.0f : f16_to_f32((uint16_t)raw[i][j].s);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          f32x4 d = F == kF4 ? acc[m][j] : start[m];
+          d = mfma(xr[i][m][0], w0, d);
+          d = mfma(xr[i][m][1], w1, d);
+          if (F == kF4) {
+            acc[m][j] = d;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[m][j][e] = fmaf(d[e], s, acc[m][j][e]);
+          }
+        }
+      }
+    }
+  }
+  wave_sums<MT * NJ, kStreamWaves>(&acc[0][0], buf, wv, lane);
+  if (wv != 0) return;
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int t = t0 + 16 * m + 4 * kg + e;
+      if (t >= g.T) continue;
+      float *p = g.part + ((int64_t)split * g.T + t) * g.m.N + n0 + NJ * c;
+      if (NJ == 4) {
+        *reinterpret_cast<float4 *>(p) =
+            make_float4(acc[m][0][e], acc[m][NJ > 1][e], acc[m][NJ > 2 ? 2 : 0][e], acc[m][NJ > 3 ? 3 : 0][e]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) p[j] = acc[m][j][e];
+      }
+    }
+}
+
+template <int F, int MT, int NJ, int GB, int RT>
+__global__ void __launch_bounds__(64 * kStreamWaves) stream_kernel(StreamArgs g) {
+  constexpr int A = MT * NJ > RT ? MT * NJ : RT;
+  __shared__ f32x4 buf[kStreamWaves / 2 * A][64];
+  int b = blockIdx.x;
+  if (b < g.shrink_blocks) {
+    const int tile = b % g.shrink_tiles;
+    b /= g.shrink_tiles;
+    shrink_tile<RT, 1, kStreamWaves>(g.s, tile, b % g.s.nsub, b / g.s.nsub, buf);
+    return;
+  }
+  b -= g.shrink_blocks;
+  const int nt = g.m.N / (16 * NJ), tt = (g.T + 16 * MT - 1) / (16 * MT);
+  const int n = b % nt;
+  b /= nt;
+  stream_tile<F, MT, NJ, GB>(g, n, b % tt, b / tt, buf);
+}
+
+// y = the sum of the parts, plus the adapters.  A wavefront takes 64 columns
+// of one 16-row tile and every nsub-th request with rows there, so that one-
+// row requests run side by side; the first of them also writes the rows
+// without an adapter.
+struct CombineArgs {
+  const float *part;  // [splits][T][N]
+  int splits, nsub;
+  void *y;
+  ExpandArgs e;
+};
+template <bool F32>
+__global__ void __launch_bounds__(256) combine_parts_kernel(CombineArgs g) {
+  const int lane = threadIdx.x & 63, c = lane & 15, kg = lane >> 4;
+  const int n0 = (blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * 64;
+  if (n0 >= g.e.N) return;
+  const int t0 = blockIdx.y * 16, t1 = min(g.e.T, t0 + 16), sub = blockIdx.z;
+  uint32_t covered = 0;
+  auto rows = [&](int begin, int end, uint32_t mask, int a) {
+    f32x4 acc[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = 4 * kg + e;
+      const bool mine = (mask >> r) & 1u;
+      float4 v = make_float4(0, 0, 0, 0);
+      if (mine) {
+        const float *p = g.part + (int64_t)(t0 + r) * g.e.N + n0 + 4 * c;
+#pragma unroll 4
+        for (int s = 0; s < g.splits; ++s) {
+          const float4 o = *reinterpret_cast<const float4 *>(p + (int64_t)s * g.e.T * g.e.N);
+          v.x += o.x;
+          v.y += o.y;
+          v.z += o.z;
+          v.w += o.w;
+        }
+      }
+      acc[0][e] = v.x;
+      acc[1][e] = v.y;
+      acc[2][e] = v.z;
+      acc[3][e] = v.w;
+    }
+    if (a >= 0) {
+      constexpr int P = F32 ? 3 : 2;
+      const int rank = rank_of(g.e.rank, a, g.e.R);
+      const int t = t0 + c;
+      for (int k0 = 0; k0 < rank; k0 += 32) {
+        const int k = k0 + 8 * kg;
+        uint4 bf[4], uf[P];
+        load_b(g.e, a, n0, k, rank, bf);
+        load_u<P>(g.e, t, k, t >= begin && t < end && k < rank, uf);
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j] = mfma(uf[p], bf[j], acc[j]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = 4 * kg + e;
+      if ((mask >> r) & 1u)
+        store4<F32>(g.y, (int64_t)(t0 + r) * g.e.N + n0 + 4 * c, acc[0][e], acc[1][e], acc[2][e],
+                    acc[3][e]);
+    }
+  };
+  if (g.e.u) {
+    for_requests(g.e.q, t0, t1, [&](int ordinal, int begin, int end, int a) {
+      const uint32_t mask = ((1u << (end - t0)) - 1u) & ~((1u << (begin - t0)) - 1u);
+      covered |= mask;
+      if (ordinal % g.nsub == sub) rows(begin, end, mask, a);
+    });
+  }
+  const uint32_t rest = ((1u << (t1 - t0)) - 1u) & ~covered;
+  if (sub == 0 && rest) rows(0, 0, rest, -1);
 }
 
 // ----------------------------------------------------------------- finish
@@ -652,23 +933,7 @@ __global__ void __launch_bounds__(256) grads_kernel(GradsArgs a) {
       }
     }
   }
-#pragma unroll
-  for (int half = 2; half > 0; half >>= 1) {
-    __syncthreads();
-    if (wv >= half && wv < 2 * half) {
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) buf[((wv - half) * RT + r) * 8 + j][lane] = acc[r][j];
-    }
-    __syncthreads();
-    if (wv < half) {
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[r][j] += buf[(wv * RT + r) * 8 + j][lane];
-    }
-  }
+  wave_sums<RT * 8, 4>(&acc[0][0], buf, wv, lane);
   if (wv != 0 || !cols) return;
   float *out = g.out + ((int64_t)split * a.n + ad) * a.R * g.F;
 #pragma unroll
@@ -746,6 +1011,28 @@ int grad_splits(int T, int N, int K, int n) {
   return (int)(s > 16 ? 16 : s);
 }
 
+// Batches of up to this many rows take the streaming path.
+constexpr int kStreamRows = 640;
+// The streaming path's tiles: columns per workgroup grow with the rows, so
+// that x is not read once per 16 columns.
+int stream_mt(int T) { return T <= 16 ? 1 : (T <= 32 ? 2 : 4); }
+int stream_splits(int T, int N, int K) {
+  const int mt = stream_mt(T);
+  const int blocks = N / (16 * mt) * ((T + 16 * mt - 1) / (16 * mt));
+  int s = 384 / blocks;
+  const int most = K / 64 / kStreamWaves;
+  if (s > most) s = most;
+  return s < 1 ? 1 : (s > 8 ? 8 : s);
+}
+
+int stream_shrink_splits(int T, int F) {
+  // a run of 64-wide blocks per wavefront
+  int s = 64 / ((T + 15) / 16);
+  const int most = (F / 64 + kStreamWaves - 1) / kStreamWaves;
+  if (s > most) s = most;
+  return s < 1 ? 1 : (s > 8 ? 8 : s);
+}
+
 struct Carve {
   char *p;
   size_t used = 0;
@@ -765,7 +1052,8 @@ struct Work {
   uint16_t *at, *bt, *planes_u, *planes_v;
   int32_t *owner;
   float *pa, *pb;
-  int su, sv, sg, Tp, R32;
+  float *part;
+  int su, sv, sg, sp, Tp, R32;
 };
 // Regions of the workspace; n = R = 0 without adapters.
 size_t carve(const Layer &L, int matrix, int n, int R, int T, bool backward, void *ws, Work *w) {
@@ -776,8 +1064,14 @@ size_t carve(const Layer &L, int matrix, int n, int R, int T, bool backward, voi
   o.Tp = (T + 63) / 64 * 64;
   o.su = shrink_splits(T, (int)K);
   o.sv = shrink_splits(T, (int)N);
-  o.plane = c.take<uint16_t>(N * K);
-  if (!backward) o.sc = c.take<float>(N * K / 64);
+  if (!backward && T <= kStreamRows) {
+    o.sp = stream_splits(T, (int)N, (int)K);
+    o.su = stream_shrink_splits(T, (int)K);
+    o.part = c.take<float>((size_t)o.sp * T * N);
+  } else {
+    o.plane = c.take<uint16_t>(N * K);
+    if (!backward) o.sc = c.take<float>(N * K / 64);
+  }
   if (n) {
     o.part_u = c.take<float>((size_t)o.su * T * o.R32);
     if (backward) {
@@ -799,12 +1093,8 @@ size_t carve(const Layer &L, int matrix, int n, int R, int T, bool backward, voi
   return c.used;
 }
 
-// Sub-tiles of requests that shrink spreads over workgroups: only short
-// batches hold many requests per tile.
-int shrink_nsub(int T, int n_req) {
-  if (T > 1024 || n_req < 2) return 1;
-  return n_req < 16 ? n_req : 16;
-}
+// Workgroups (per tile) that the requests of a tile are spread over.
+int spread(int rows, int n_req) { return n_req < rows ? n_req : rows; }
 
 int launch_shrink(const ShrinkArgs &a, const ShrinkArgs &b, hipStream_t s) {
   const dim3 grid((a.T + 63) / 64, a.nsub, a.splits + b.splits);
@@ -819,6 +1109,24 @@ int launch_gemm(const GemmArgs &g, hipStream_t s) {
   const dim3 grid((g.N + 127) / 128, (g.T + 127) / 128);
   launch_k(COLI_K_PROJECT_GEMM, gemm_kernel<128, 128, 64, SCALED, F32>, grid, dim3(256), 0, s, g);
   return hip_status(hipGetLastError());
+}
+
+template <int F, int RT>
+int launch_stream(const StreamArgs &g, hipStream_t s) {
+  const int mt = stream_mt(g.T);
+  const unsigned grid = g.shrink_blocks +
+                        g.m.N / (16 * mt) * ((g.T + 16 * mt - 1) / (16 * mt)) * g.splits;
+  const dim3 b(64 * kStreamWaves);
+  if (mt == 1) launch_k(COLI_K_PROJECT_STREAM, stream_kernel<F, 1, 1, 4, RT>, dim3(grid), b, 0, s, g);
+  else if (mt == 2) launch_k(COLI_K_PROJECT_STREAM, stream_kernel<F, 2, 2, 2, RT>, dim3(grid), b, 0, s, g);
+  else launch_k(COLI_K_PROJECT_STREAM, stream_kernel<F, 4, 4, 1, RT>, dim3(grid), b, 0, s, g);
+  return hip_status(hipGetLastError());
+}
+template <int F>
+int launch_stream_rank(const StreamArgs &g, int R32, hipStream_t s) {
+  if (R32 <= 32) return launch_stream<F, 2>(g, s);
+  if (R32 <= 64) return launch_stream<F, 4>(g, s);
+  return launch_stream<F, 8>(g, s);
 }
 
 Requests requests_of(const coli_moe_adapters_t *ad, const coli_moe_requests_t *rq) {
@@ -842,36 +1150,59 @@ int launch_project(const Layer &L, int expert, int matrix, const coli_moe_adapte
   const Matrix m = matrix_of(L, expert, matrix);
   Work w;
   carve(L, matrix, ad ? ad->n_adapters : 0, ad ? ad->max_rank : 0, T, false, ws, &w);
-  const unsigned pb = (unsigned)(((int64_t)m.N * m.K / 8 + 255) / 256);
   const int fmt = format_of(L);
+  const bool f32 = y_dtype == COLI_OUT_F32;
+  ExpandArgs e = {};
+  e.T = T;
+  e.N = m.N;
+  ShrinkArgs sh = {};
+  if (ad) {
+    e.q = requests_of(ad, rq);
+    e.u = w.part_u;
+    e.b = ad->b;
+    e.rank = ad->rank;
+    e.R = ad->max_rank;
+    e.R32 = w.R32;
+    e.splits = w.su;
+    sh = {x, ad->a, ad->rank, ad->scale, e.q, w.part_u, T, m.K, e.R, e.R32, w.su, 1};
+  }
+  int rc;
+  if (T <= kStreamRows) {
+    StreamArgs g = {};
+    g.m = m;
+    g.x = x;
+    g.part = w.part;
+    g.T = T;
+    g.splits = w.sp;
+    g.per = (m.K / 64 + kStreamWaves * w.sp - 1) / (kStreamWaves * w.sp);
+    g.shrink_tiles = (T + 15) / 16;
+    g.s = sh;
+    CombineArgs c = {};
+    c.part = w.part;
+    c.splits = w.sp;
+    c.nsub = 1;
+    c.y = y;
+    c.e = e;
+    if (ad) {
+      c.nsub = g.s.nsub = spread(16, e.q.n);
+      g.shrink_blocks = g.shrink_tiles * g.s.nsub * w.su;
+    }
+    rc = fmt == kI4 ? launch_stream_rank<kI4>(g, w.R32, s)
+                    : (fmt == kI8 ? launch_stream_rank<kI8>(g, w.R32, s)
+                                  : launch_stream_rank<kF4>(g, w.R32, s));
+    if (rc) return rc;
+    const dim3 grid((m.N + 255) / 256, (T + 15) / 16, c.nsub);
+    if (f32) launch_k(COLI_K_PROJECT_COMBINE, combine_parts_kernel<true>, grid, dim3(256), 0, s, c);
+    else launch_k(COLI_K_PROJECT_COMBINE, combine_parts_kernel<false>, grid, dim3(256), 0, s, c);
+    return hip_status(hipGetLastError());
+  }
+  const unsigned pb = (unsigned)(((int64_t)m.N * m.K / 8 + 255) / 256);
   if (fmt == kI4) launch_k(COLI_K_PROJECT_PREP, prep_kernel<kI4>, dim3(pb), dim3(256), 0, s, m, w.plane, w.sc);
   else if (fmt == kI8) launch_k(COLI_K_PROJECT_PREP, prep_kernel<kI8>, dim3(pb), dim3(256), 0, s, m, w.plane, w.sc);
   else launch_k(COLI_K_PROJECT_PREP, prep_kernel<kF4>, dim3(pb), dim3(256), 0, s, m, w.plane, w.sc);
-  int rc = hip_status(hipGetLastError());
-  if (rc) return rc;
-  GemmArgs g = {};
-  g.x = x;
-  g.w = w.plane;
-  g.sc = w.sc;
-  g.T = T;
-  g.N = m.N;
-  g.K = m.K;
-  g.y = y;
-  if (ad) {
-    const Requests q = requests_of(ad, rq);
-    ShrinkArgs a = {x, ad->a, ad->rank, ad->scale, q, w.part_u, T, m.K, ad->max_rank, w.R32, w.su,
-                    shrink_nsub(T, q.n)};
-    ShrinkArgs none = {};
-    if ((rc = launch_shrink(a, none, s))) return rc;
-    g.q = q;
-    g.u = w.part_u;
-    g.b = ad->b;
-    g.rank = ad->rank;
-    g.R = ad->max_rank;
-    g.R32 = w.R32;
-    g.splits = w.su;
-  }
-  const bool f32 = y_dtype == COLI_OUT_F32;
+  if ((rc = hip_status(hipGetLastError()))) return rc;
+  if (ad && (rc = launch_shrink(sh, ShrinkArgs{}, s))) return rc;
+  const GemmArgs g = {x, w.plane, w.sc, T, m.N, m.K, y, e};
   if (fmt == kF4) return f32 ? launch_gemm<false, true>(g, s) : launch_gemm<false, false>(g, s);
   return f32 ? launch_gemm<true, true>(g, s) : launch_gemm<true, false>(g, s);
 }
@@ -904,7 +1235,7 @@ int launch_project_backward(const Layer &L, int expert, int matrix, const coli_m
   if ((rc = hip_status(hipGetLastError()))) return rc;
   if (ad) {
     const Requests q = p.q;
-    const int nsub = shrink_nsub(T, q.n);
+    const int nsub = T <= 1024 ? spread(16, q.n) : 1;
     const ShrinkArgs u = {x, ad->a, ad->rank, ad->scale, q, w.part_u, T, m.K, R, w.R32, w.su, nsub};
     const ShrinkArgs v = {dy, w.bt, ad->rank, ad->scale, q, w.part_v, T, m.N, R, w.R32, w.sv, nsub};
     if ((rc = launch_shrink(u, v, s))) return rc;
@@ -956,23 +1287,9 @@ int launch_project_backward(const Layer &L, int expert, int matrix, const coli_m
     }
   }
   if (!dx) return COLI_OK;
-  GemmArgs g = {};
-  g.x = dy;
-  g.w = w.plane;
-  g.T = T;
-  g.N = m.K;
-  g.K = m.N;
-  g.y = dx;
-  if (ad) {
-    g.q = p.q;
-    g.u = w.rows;
-    g.b = w.at;
-    g.rank = ad->rank;
-    g.R = R;
-    g.R32 = w.R32;
-    g.splits = 1;
-  }
-  return launch_gemm<false, false>(g, s);
+  ExpandArgs e = {};
+  if (ad) e = {p.q, w.rows, w.at, ad->rank, T, m.K, R, w.R32, 1};
+  return launch_gemm<false, false>({dy, w.plane, nullptr, T, m.K, m.N, dx, e}, s);
 }
 
 }  // namespace coli

@@ -40,7 +40,8 @@ struct Requests {
 template <class F>
 COLI_DEV void for_requests(const Requests &q, int lo, int hi, F f) {
   const int lane = threadIdx.x & 63;
-  int s = max(0, last_at_or_before(q.off, q.n + 1, lo));
+  // up to 64 requests are one step anyway
+  int s = q.n <= 64 ? 0 : max(0, last_at_or_before(q.off, q.n + 1, lo));
   int ordinal = 0;
   for (; s < q.n; s += 64) {
     const int i = min(s + lane, q.n - 1);
