@@ -35,18 +35,38 @@ constexpr int kMaxFinish = 512;  // workgroups of the second kernel
 constexpr int kSoloRows = 64;    // up to here one workgroup does everything
 constexpr int kCols = 16;        // experts per item of the second kernel
 
+// Reductions over aligned groups of W lanes, the result in every lane: DPP
+// moves within 16 lanes (neighbours, pairs, mirrored halves, mirrored row),
+// then the row and half swaps, no LDS round trips.
+template <int CTRL>
+COLI_DEV float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+template <int W, class Op>
+COLI_DEV float reduce_w(float v, Op op) {
+  if (W >= 2) v = op(v, dpp<0xB1>(v));    // quad_perm 1,0,3,2
+  if (W >= 4) v = op(v, dpp<0x4E>(v));    // quad_perm 2,3,0,1
+  if (W >= 8) v = op(v, dpp<0x141>(v));   // row_half_mirror
+  if (W >= 16) v = op(v, dpp<0x140>(v));  // row_mirror
+  if (W >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  if (W >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  return v;
+}
 template <int W>
 COLI_DEV float sum_w(float v) {
-#pragma unroll
-  for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
+  return reduce_w<W>(v, [](float a, float b) { return a + b; });
 }
 template <int W>
 COLI_DEV float max_w(float v) {
-#pragma unroll
-  for (int o = W / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-  return v;
+  return reduce_w<W>(v, [](float a, float b) { return fmaxf(a, b); });
 }
+COLI_DEV float rcp(float v) { return __builtin_amdgcn_rcpf(v); }  // 1 ulp
 
 template <int V>
 COLI_DEV void load_v(const float *p, float *out) {
@@ -81,47 +101,58 @@ COLI_DEV void load_row(const float *__restrict__ row, int E, int gl, float (&l)[
   }
 }
 
-// exp(-|l|), from which both the sigmoid and its complement follow without
-// cancellation.
-COLI_DEV float sig_part(float l) { return __expf(-fabsf(l)); }
-COLI_DEV float sig(float l, float q) { return (l >= 0.0f ? 1.0f : q) / (1.0f + q); }
-COLI_DEV float one_minus_sig(float l, float q) { return (l >= 0.0f ? q : 1.0f) / (1.0f + q); }
-
-// Unnormalised probability of an entry with logit l, in a row whose largest
-// logit is m: exp(l - m), or the sigmoid -- where all logits are negative
-// times exp(-m), so that the row's sum does not underflow.
-template <bool SIGMOID>
-COLI_DEV float score(float l, float m, float e1) {
-  if (!SIGMOID) return e1;
-  const float q = sig_part(l);
-  return m >= 0.0f ? sig(l, q) : e1 / (1.0f + q);
+// Sigmoid and its complement without cancellation, from one exponential.
+struct Sig {
+  float s, c;  // sig(l), 1 - sig(l)
+  float r;     // 1 / (1 + exp(-|l|)), which is sig(l) exp(-l) where l < 0
+};
+COLI_DEV Sig sigmoid(float l) {
+  const float q = __expf(-fabsf(l));
+  const float r = rcp(1.0f + q);
+  return {l >= 0.0f ? r : q * r, l >= 0.0f ? q * r : r, r};
 }
 
-// p (normalised probabilities) and the log-sum-exp of a row.  A row without
-// a finite logit has p = 0 and lse = 0.
-template <int W, int C, int V, bool SIGMOID>
-COLI_DEV void row_probs(const float (&l)[C * V], float (&p)[C * V], float &m, float &sum,
-                        float &lse) {
-  m = -INFINITY;
+// Unnormalised probability of an entry with logit l, in a row whose largest
+// logit is m: e1 = exp(l - m), or the sigmoid -- where all logits are
+// negative times exp(-m), so that the row's sum does not underflow.
+template <bool SIGMOID>
+COLI_DEV float score(const Sig &g, float m, float e1) {
+  return !SIGMOID ? e1 : (m >= 0.0f ? g.s : e1 * g.r);
+}
+
+// A row's probabilities p, exponentials e1 = exp(l - m), sigmoid complements
+// and log-sum-exp.  A row without a finite logit has p = e1 = 0 and lse = 0.
+template <int N>
+struct Row {
+  float p[N], e1[N], c[N];
+  float m, inv, lse;  // inv: 1 / sum of e1
+};
+template <int W, int N, bool SIGMOID>
+COLI_DEV void row_probs(const float (&l)[N], Row<N> &o) {
+  float m = l[0];
 #pragma unroll
-  for (int i = 0; i < C * V; ++i) m = fmaxf(m, l[i]);
+  for (int i = 1; i < N; ++i) m = fmaxf(m, l[i]);
   m = max_w<W>(m);
   const bool any = m > -INFINITY;
   float s = 0.0f, z = 0.0f;
 #pragma unroll
-  for (int i = 0; i < C * V; ++i) {
-    const float e1 = any ? __expf(l[i] - m) : 0.0f;
-    s += e1;
-    p[i] = any ? score<SIGMOID>(l[i], m, e1) : 0.0f;
-    if (SIGMOID) z += p[i];
+  for (int i = 0; i < N; ++i) {
+    o.e1[i] = any ? __expf(l[i] - m) : 0.0f;
+    s += o.e1[i];
+    Sig g = {};
+    if (SIGMOID) g = sigmoid(l[i]);
+    o.c[i] = g.c;
+    o.p[i] = any ? score<SIGMOID>(g, m, o.e1[i]) : 0.0f;
+    if (SIGMOID) z += o.p[i];
   }
-  sum = sum_w<W>(s);
-  if (SIGMOID) z = sum_w<W>(z);
-  else z = sum;
-  lse = any ? m + __logf(sum) : 0.0f;
-  const float inv = any ? 1.0f / z : 0.0f;
+  s = sum_w<W>(s);
+  z = SIGMOID ? sum_w<W>(z) : s;
+  o.m = m;
+  o.inv = any ? rcp(s) : 0.0f;
+  o.lse = any ? m + __logf(s) : 0.0f;
+  const float inv = any ? rcp(z) : 0.0f;
 #pragma unroll
-  for (int i = 0; i < C * V; ++i) p[i] *= inv;
+  for (int i = 0; i < N; ++i) o.p[i] *= inv;
 }
 
 // ---------------------------------------------------------------- forward
@@ -158,22 +189,32 @@ COLI_DEV int seq_end(const FwdArgs &g, int s) {
 struct FinShared {
   float p[kFwdThreads];
   int c[kFwdThreads];
-  double d[kFwdThreads];
   int n[kFwdThreads];
+  double d[kFwdThreads / 64];
+  int i[kFwdThreads / 64];
   int last;
 };
 
-template <typename X>
-COLI_DEV X block_sum(X v, X *buf) {
-  buf[threadIdx.x] = v;
-  __syncthreads();
-  for (int o = kFwdThreads / 2; o > 0; o >>= 1) {
-    if ((int)threadIdx.x < o) buf[threadIdx.x] += buf[threadIdx.x + o];
-    __syncthreads();
+// Sums over the workgroup, the same in every thread.
+COLI_DEV void block_sums(double &v, int &n, FinShared &sh) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    v += __shfl_xor(v, o, 64);
+    n += __shfl_xor(n, o, 64);
   }
-  const X r = buf[0];
   __syncthreads();
-  return r;
+  if ((threadIdx.x & 63) == 0) {
+    sh.d[threadIdx.x >> 6] = v;
+    sh.i[threadIdx.x >> 6] = n;
+  }
+  __syncthreads();
+  v = 0.0;
+  n = 0;
+#pragma unroll
+  for (int w = 0; w < kFwdThreads / 64; ++w) {
+    v += sh.d[w];
+    n += sh.i[w];
+  }
 }
 
 // Finishes the sequences (items of kCols experts of one sequence): adds the
@@ -198,12 +239,11 @@ __device__ void finish_sequences(const FwdArgs &g, FinShared &sh, int block, int
     if (!empty && tile0 != tile1) {
       // rows of partials: tile0 (its last sequence, or its first if the
       // sequence starts with the tile), then the first of every later tile
+#pragma unroll 4
       for (int i = tile0 + rg; i <= tile1; i += kRows) {
         const int64_t row = 2 * (int64_t)i + (i == tile0 && b != tile0 * g.tile ? 1 : 0);
-        if (e < g.E) {
-          p += g.part_p[row * g.E + e];
-          c += g.part_c[row * g.E + e];
-        }
+        p += g.part_p[row * g.E + min(e, g.E - 1)];
+        c += g.part_c[row * g.E + min(e, g.E - 1)];
         n += g.part_n[row];
       }
       sh.p[tid] = p;
@@ -238,8 +278,7 @@ __device__ void finish_sequences(const FwdArgs &g, FinShared &sh, int block, int
       if (e == 0 && n) ++live;
     }
   }
-  term = block_sum(term, sh.d);
-  live = block_sum(live, sh.n);
+  block_sums(term, live, sh);
   if (!solo) {
     // the partial sums pass between workgroups of different L2s: device
     // scope on both sides of the ticket
@@ -258,8 +297,7 @@ __device__ void finish_sequences(const FwdArgs &g, FinShared &sh, int block, int
       term += __hip_atomic_load(&g.fin_term[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       live += __hip_atomic_load(&g.fin_live[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    term = block_sum(term, sh.d);
-    live = block_sum(live, sh.n);
+    block_sums(term, live, sh);
   }
   double z = 0.0;
   int n = 0;
@@ -267,8 +305,7 @@ __device__ void finish_sequences(const FwdArgs &g, FinShared &sh, int block, int
     z += g.tile_z[i];
     n += g.tile_n[i];
   }
-  z = block_sum(z, sh.d);
-  n = block_sum(n, sh.n);
+  block_sums(z, n, sh);
   if (tid == 0) {
     g.loss[0] = live ? (float)(term * g.E / g.k / live) : 0.0f;
     g.loss[1] = n ? (float)(z / n) : 0.0f;
@@ -310,21 +347,29 @@ __global__ void __launch_bounds__(kFwdThreads) balance_kernel(FwdArgs g) {
       if (tid == 0) counted = 0;
       __syncthreads();
       int mine = 0;
-      for (int t = pos + grp; t < end; t += G) {
-        if (g.valid && !g.valid[t]) continue;
-        float l[C * V], p[C * V], m, sum, lse;
-        load_row<W, C, V>(g.logits + (int64_t)t * E, E, gl, l);
-        row_probs<W, C, V, SIGMOID>(l, p, m, sum, lse);
+      float l[C * V];
+      int t = pos + grp;
+      if (t < end) load_row<W, C, V>(g.logits + (int64_t)t * E, E, gl, l);
+      for (; t < end; t += G) {
+        float next[C * V];  // the next row, on its way while this one is summed
+        const int tn = min(t + G, end - 1);
+        load_row<W, C, V>(g.logits + (int64_t)tn * E, E, gl, next);
+        if (!g.valid || g.valid[t]) {
+          for (int j = gl; j < g.k; j += W) {
+            const int e = g.idx[(int64_t)t * g.k + j];
+            if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
+          }
+          Row<C * V> r;
+          row_probs<W, C * V, SIGMOID>(l, r);
 #pragma unroll
-        for (int i = 0; i < C * V; ++i) acc[i] += p[i];
-        for (int j = gl; j < g.k; j += W) {
-          const int e = g.idx[(int64_t)t * g.k + j];
-          if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
+          for (int i = 0; i < C * V; ++i) acc[i] += r.p[i];
+          if (gl == 0) {
+            zsum += (double)r.lse * (double)r.lse;
+            ++mine;
+          }
         }
-        if (gl == 0) {
-          zsum += (double)lse * (double)lse;
-          ++mine;
-        }
+#pragma unroll
+        for (int i = 0; i < C * V; ++i) l[i] = next[i];
       }
       if (gl == 0 && mine) atomicAdd(&counted, mine);
 #pragma unroll
@@ -355,7 +400,8 @@ __global__ void __launch_bounds__(kFwdThreads) balance_kernel(FwdArgs g) {
     }
     pos = end;
   }
-  zsum = block_sum(zsum, fin.d);
+  int unused = 0;
+  block_sums(zsum, unused, fin);
   if (tid == 0) {
     g.tile_z[blockIdx.x] = zsum;
     g.tile_n[blockIdx.x] = ntile;
@@ -393,71 +439,93 @@ struct BwdArgs {
 
 constexpr int kBwdThreads = 256;
 
-// Gradients of the routing weights with respect to the chosen logits, added
-// into the row's LDS entries; returns sum_j g_j w_j of the plain softmax.
-template <int W, bool SIGMOID, bool RENORM>
-COLI_DEV float route_part(const BwdArgs &g, int64_t t, int gl, float m, float inv, float *row) {
-  const float *lrow = g.logits + t * g.E;
-  const int32_t *idx = g.idx + t * g.k;
-  const float *dw = g.d_w + t * g.k;
-  const float c = g.routed_scale;
+// A row's choices, KL to a lane: expert (-1: none) and gradient of its weight.
+template <int KL>
+struct Chosen {
+  int e[KL];
+  float d[KL];
+};
+template <int W, int KL>
+COLI_DEV void load_chosen(const BwdArgs &g, int64_t t, int gl, Chosen<KL> &o) {
+#pragma unroll
+  for (int i = 0; i < KL; ++i) {
+    const int j = gl + W * i;
+    o.e[i] = -1;
+    o.d[i] = 0.0f;
+    if (j < g.k) {
+      const int e = g.idx[t * g.k + j];
+      o.e[i] = e >= 0 && e < g.E ? e : -1;
+      o.d[i] = g.d_w[t * g.k + j];
+    }
+  }
+}
+
+// Adds the gradients of the routing weights with respect to the chosen
+// logits l into the row's LDS entries (an LDS add, so that an expert named
+// twice gets both); returns sum_j g_j w_j of the plain softmax, whose
+// p_j-weighted part every entry of the row loses.
+template <int W, int KL, bool SIGMOID, bool RENORM>
+COLI_DEV float route_part(const Chosen<KL> &ch, const float (&l)[KL], float c, float m, float inv,
+                          float *row) {
   float out = 0.0f;
   if (!RENORM) {
-    for (int j = gl; j < g.k; j += W) {
-      const int e = idx[j];
-      if (e < 0 || e >= g.E) continue;
-      const float l = lrow[e];
-      float d;
+#pragma unroll
+    for (int i = 0; i < KL; ++i) {
+      if (ch.e[i] < 0) continue;
+      float d = c * ch.d[i];
       if (SIGMOID) {
-        const float q = sig_part(l);
-        d = c * dw[j] * sig(l, q) * one_minus_sig(l, q);
+        const Sig s = sigmoid(l[i]);
+        d *= s.s * s.c;
       } else {
-        d = c * dw[j] * __expf(l - m) * inv;
+        d *= __expf(l[i] - m) * inv;
         out += d;
       }
-      atomicAdd(&row[e], d);
+      atomicAdd(&row[ch.e[i]], d);
     }
     return SIGMOID ? 0.0f : sum_w<W>(out);
   }
   float ms = -INFINITY;
-  for (int j = gl; j < g.k; j += W) {
-    const int e = idx[j];
-    if (e >= 0 && e < g.E) ms = fmaxf(ms, lrow[e]);
-  }
+#pragma unroll
+  for (int i = 0; i < KL; ++i)
+    if (ch.e[i] >= 0) ms = fmaxf(ms, l[i]);
   ms = max_w<W>(ms);
-  if (!(ms > -INFINITY)) return 0.0f;
-  float z = 0.0f, gw = 0.0f;
-  for (int j = gl; j < g.k; j += W) {
-    const int e = idx[j];
-    if (e < 0 || e >= g.E) continue;
-    const float w = score<SIGMOID>(lrow[e], ms, __expf(lrow[e] - ms));
-    z += w;
-    gw += w * dw[j];
+  const bool any = ms > -INFINITY;
+  float w[KL], comp[KL], z = 0.0f, gw = 0.0f;
+#pragma unroll
+  for (int i = 0; i < KL; ++i) {
+    w[i] = comp[i] = 0.0f;
+    if (ch.e[i] < 0 || !any) continue;
+    Sig s = {};
+    if (SIGMOID) s = sigmoid(l[i]);
+    comp[i] = SIGMOID ? s.c : 1.0f;
+    w[i] = score<SIGMOID>(s, ms, __expf(l[i] - ms));
+    z += w[i];
+    gw += w[i] * ch.d[i];
   }
-  z = 1.0f / sum_w<W>(z);
-  gw = sum_w<W>(gw) * z;
-  for (int j = gl; j < g.k; j += W) {
-    const int e = idx[j];
-    if (e < 0 || e >= g.E) continue;
-    const float l = lrow[e];
-    float d = c * score<SIGMOID>(l, ms, __expf(l - ms)) * z * (dw[j] - gw);
-    if (SIGMOID) d *= one_minus_sig(l, sig_part(l));
-    atomicAdd(&row[e], d);
-  }
+  z = sum_w<W>(z);
+  gw = sum_w<W>(gw);
+  const float iz = any ? rcp(z) : 0.0f;
+  gw *= iz;
+#pragma unroll
+  for (int i = 0; i < KL; ++i)
+    if (ch.e[i] >= 0) atomicAdd(&row[ch.e[i]], c * w[i] * iz * comp[i] * (ch.d[i] - gw));
   return 0.0f;
 }
 
 template <int W, int C, int V, bool SIGMOID, bool RENORM>
 __global__ void __launch_bounds__(kBwdThreads) route_backward_kernel(BwdArgs g) {
-  constexpr int G = 64 / W;     // rows of a wavefront in flight
+  constexpr int G = 64 / W;  // rows of a wavefront in flight
   constexpr int S = W * C * V;
-  __shared__ float rows[kBwdThreads / W][S];
+  constexpr int KL = W >= 32 ? 1 : (W == 16 ? 2 : 4);  // choices per lane: k <= min(E, 32)
+  __shared__ __align__(16) float grads[kBwdThreads / W][S];
+  __shared__ __align__(16) float logit[kBwdThreads / W][S];
   const int lane = threadIdx.x & 63, gl = lane % W, grp = lane / W;
   const int wave = __builtin_amdgcn_readfirstlane(blockIdx.x * (kBwdThreads / 64) + (threadIdx.x >> 6));
   const int E = g.E;
-  float *row = rows[threadIdx.x / W];
+  float *row = grads[threadIdx.x / W], *lrow = logit[threadIdx.x / W];
   const bool balance = g.counts != nullptr;
-  // rows are cleared once here and again by whoever read them
+  const bool full = balance || (!SIGMOID && !RENORM);  // needs the whole row
+  // gradient rows are cleared once here and again by whoever read them
   for (int i = gl; i < S; i += W) row[i] = 0.0f;
   const int64_t first = (int64_t)wave * g.rows;
   if (first >= g.T) return;
@@ -467,11 +535,22 @@ __global__ void __launch_bounds__(kBwdThreads) route_backward_kernel(BwdArgs g) 
     bc = g.d_loss[0] / (float)max(1, g.totals[1]) * (float)E / (float)g.k;
     zc = 2.0f * g.d_loss[1] / (float)max(1, g.totals[0]);
   }
+  // the next row's inputs are on their way while this one is worked on
+  float l[C * V];
+  Chosen<KL> ch = {};
+  int live = 0;
+  auto fetch = [&](int t, float (&lo)[C * V], Chosen<KL> &co, int &vo) {
+    t = min(t, row1 - 1);
+    if (full) load_row<W, C, V>(g.logits + (int64_t)t * E, E, gl, lo);
+    if (g.d_w) load_chosen<W, KL>(g, t, gl, co);
+    vo = g.valid ? g.valid[t] : 1;
+  };
   for (int pos = row0; pos < row1;) {
     int s = 0, end = g.T;
     float f[C * V];
 #pragma unroll
     for (int i = 0; i < C * V; ++i) f[i] = 0.0f;
+    fetch(pos + grp, l, ch, live);
     if (balance) {
       if (g.off) {
         s = last_at_or_before(g.off, g.n_seq + 1, pos);
@@ -492,43 +571,56 @@ __global__ void __launch_bounds__(kBwdThreads) route_backward_kernel(BwdArgs g) 
     }
     end = min(max(end, pos + 1), row1);
     for (int t = pos + grp; t < end; t += G) {
-      const bool live = !balance || (s >= 0 && !(g.valid && !g.valid[t]));
+      float ln[C * V];
+      Chosen<KL> cn = {};
+      int vn;
+      fetch(t + G, ln, cn, vn);
+      const bool counts = !balance || (s >= 0 && live);
       float d[C * V];
 #pragma unroll
       for (int i = 0; i < C * V; ++i) d[i] = 0.0f;
-      if (live) {
-        const bool full = balance || (!SIGMOID && !RENORM);
-        float p[C * V], m = 0.0f, inv = 0.0f;
+      if (counts) {
+        Row<C * V> r;
+        r.m = r.inv = 0.0f;
         if (full) {
-          float l[C * V], sum, lse;
-          load_row<W, C, V>(g.logits + (int64_t)t * E, E, gl, l);
-          row_probs<W, C, V, SIGMOID>(l, p, m, sum, lse);
-          inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+          row_probs<W, C * V, SIGMOID>(l, r);
           if (balance) {
             float dot = 0.0f;
 #pragma unroll
-            for (int i = 0; i < C * V; ++i) dot += f[i] * p[i];
+            for (int i = 0; i < C * V; ++i) dot += f[i] * r.p[i];
             dot = sum_w<W>(dot);
-            const float zr = zc * lse * inv;
+            const float zr = zc * r.lse * r.inv;
 #pragma unroll
             for (int i = 0; i < C * V; ++i) {
-              float b = p[i] * (f[i] - dot);
-              if (SIGMOID) b *= one_minus_sig(l[i], sig_part(l[i]));
-              d[i] = b + (sum > 0.0f ? zr * __expf(l[i] - m) : 0.0f);
+              const float b = r.p[i] * (f[i] - dot);
+              d[i] = (SIGMOID ? b * r.c[i] : b) + zr * r.e1[i];
             }
           }
         }
         if (g.d_w) {
-          const float gw = route_part<W, SIGMOID, RENORM>(g, t, gl, m, inv, row);
+          float lc[KL];
+          if (full) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) store_v<V>(lrow + V * (gl + W * c), l + V * c);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          }
+#pragma unroll
+          for (int i = 0; i < KL; ++i) {
+            const int e = max(ch.e[i], 0);
+            lc[i] = full ? lrow[e] : g.logits[(int64_t)t * E + e];
+          }
+          const float gw = route_part<W, KL, SIGMOID, RENORM>(ch, lc, g.routed_scale, r.m, r.inv, row);
           __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
           for (int c = 0; c < C; ++c) {
-            const int e = V * (gl + W * c);
+            float *p = row + V * (gl + W * c);
+            float v4[V], zero[V] = {};
+            load_v<V>(p, v4);
+            store_v<V>(p, zero);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-              d[V * c + v] += row[e + v];
-              if (!SIGMOID && !RENORM) d[V * c + v] -= p[V * c + v] * gw;
-              row[e + v] = 0.0f;
+              d[V * c + v] += v4[v];
+              if (!SIGMOID && !RENORM) d[V * c + v] -= r.p[V * c + v] * gw;
             }
           }
           __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -539,6 +631,10 @@ __global__ void __launch_bounds__(kBwdThreads) route_backward_kernel(BwdArgs g) 
         const int e = V * (gl + W * c);
         if (e < E) store_v<V>(g.d_logits + (int64_t)t * E + e, d + V * c);
       }
+#pragma unroll
+      for (int i = 0; i < C * V; ++i) l[i] = ln[i];
+      ch = cn;
+      live = vn;
     }
     pos = end;
   }
