@@ -102,6 +102,8 @@ COLI_DEV void wave_sums(f32x4 *acc, f32x4 (*buf)[64], int wv, int lane) {
   }
 }
 
+constexpr int kMaxSplits = 4;  // parts of a sum along K
+
 struct Adapters {
   const uint16_t *a, *b;  // [n][R][K], [n][N][R]
   const int32_t *rank;    // [n] or NULL
@@ -113,7 +115,7 @@ COLI_DEV int rank_of(const int32_t *rank, int a, int R) {
 }
 
 // One matrix of the container.
-enum { kI4 = 0, kI8 = 1, kF4 = 2 };
+enum { kI4 = 0, kI8 = 1, kF4 = 2, kBF = 3 };  // kBF: a bf16 plane instead of codes
 struct Matrix {
   const uint8_t *q;   // codes, row n at n * row_bytes
   const uint8_t *sc;  // scales: fp16 per 64, or E8M0 per 32 (kF4)
@@ -283,6 +285,18 @@ struct ShrinkArgs {
   int T, F, R, R32, splits, nsub;
 };
 
+// One of two, field by field: a reference chosen at run time would have the
+// compiler copy both to scratch memory and read every use from there.
+COLI_DEV ShrinkArgs pick(const ShrinkArgs &a, const ShrinkArgs &b, bool second) {
+  ShrinkArgs g = a;  // masks, sizes and the rest are the same for both
+  g.z = second ? b.z : a.z;
+  g.m = second ? b.m : a.m;
+  g.part = second ? b.part : a.part;
+  g.F = second ? b.F : a.F;
+  g.splits = second ? b.splits : a.splits;
+  return g;
+}
+
 // One workgroup per tile of 16 MI rows, split and residue of the tile's
 // requests modulo nsub (so that a tile of many one-row requests spreads over
 // many workgroups).  Its NW wavefronts take the split's 64-wide k blocks in
@@ -342,13 +356,88 @@ COLI_DEV void shrink_tile(const ShrinkArgs &g, int tile, int sub, int split, f32
   });
 }
 
+// Long requests: z and the adapter staged in LDS, 128 k at a time, two stages
+// in turn, for 64 rows; each of the four wavefronts takes 16 of them against
+// all ranks.  (Operand loads straight from memory touch 16 rows per
+// instruction, which the memory pipeline takes in four lanes at a time: they
+// held this pass at 2 TB/s.)  16-byte chunk q of a row is kept at q ^ 2 (row &
+// 7), so that the chunks that LDS serves together fall on distinct banks.
+// Rows of z outside the request are only copied in groups of four.
 template <int RT>
 __global__ void __launch_bounds__(256) shrink_kernel(ShrinkArgs g0, ShrinkArgs g1) {
-  __shared__ f32x4 buf[2 * 4 * RT][64];
-  // z: the first operand's splits, then the second's
-  const bool second = (int)blockIdx.z >= g0.splits;
-  const ShrinkArgs &g = second ? g1 : g0;
-  shrink_tile<RT, 4, 4>(g, blockIdx.x, blockIdx.y, second ? blockIdx.z - g0.splits : blockIdx.z, buf);
+  constexpr int kRowsA = 64, kChunks = 16, kRows = kRowsA + 16 * RT;
+  constexpr int LD = kRows / 16;  // DMA instructions (four rows) of a wavefront per stage
+  __shared__ uint4 stage0[kRows * kChunks], stage1[kRows * kChunks];
+  const bool second = (int)blockIdx.z >= g0.splits;  // the first operand's splits, then the second's
+  const ShrinkArgs g = pick(g0, g1, second);
+  const int split = second ? blockIdx.z - g0.splits : blockIdx.z;
+  const int lane = threadIdx.x & 63, c = lane & 15, kg = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t0 = blockIdx.x * 64, t1 = min(g.T, t0 + 64);
+  const int nb = g.F / 64, per = (nb + g.splits - 1) / g.splits;
+  const int b0 = split * per, b1 = min(nb, b0 + per), nst = (b1 - b0 + 1) / 2;
+  for_requests(g.q, t0, t1, [&](int ordinal, int begin, int end, int a) {
+    if (ordinal % g.nsub != (int)blockIdx.y) return;
+    const int rank = rank_of(g.rank, a, g.R);
+    const uint16_t *src[LD];
+#pragma unroll
+    for (int i = 0; i < LD; ++i) {
+      const int row = (wv * LD + i) * 4 + (lane >> 4), q = (lane & 15) ^ (2 * (row & 7));
+      const uint16_t *p = (wv * LD + i) * 4 < kRowsA
+                              ? g.z + (int64_t)min(t0 + row, g.T - 1) * g.F
+                              : g.m + ((int64_t)a * g.R + min(row - kRowsA, g.R - 1)) * g.F;
+      src[i] = p + 64 * b0 + 8 * q;
+    }
+    auto issue = [&](uint4 *to, int st) {
+      // an odd last stage copies its one block twice; the copy is not used
+      const bool half = b0 + 2 * st + 1 >= b1;
+#pragma unroll
+      for (int i = 0; i < LD; ++i) {
+        const int r0 = (wv * LD + i) * 4, row = r0 + (lane >> 4);
+        if (r0 < kRowsA && (t0 + r0 + 4 <= begin || t0 + r0 >= end)) continue;
+        const int back = half && (((lane & 15) ^ (2 * (row & 7))) >> 3) ? 64 : 0;
+        dma16(src[i] + 128 * st - back, to + r0 * kChunks);
+      }
+    };
+    f32x4 acc[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[r] = f32x4{0, 0, 0, 0};
+    // rows of other requests and ranks past the adapter's multiply whatever is
+    // there: a sum depends on its own row and rank alone, and theirs are not used
+    auto compute = [&](const uint4 *A, int st) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if (s == 2 && b0 + 2 * st + 1 >= b1) break;
+        const int q = (kg + 4 * s) ^ (2 * (c & 7));
+        const uint4 zf = A[(16 * wv + c) * kChunks + q];
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          acc[r] = mfma(zf, A[(kRowsA + 16 * r + c) * kChunks + q], acc[r]);
+      }
+    };
+    __syncthreads();  // the buffers may still be read for the request before
+    if (nst > 0) issue(stage0, 0);
+    for (int st = 0; st < nst; st += 2) {
+      wait_dma();
+      __syncthreads();
+      if (st + 1 < nst) issue(stage1, st + 1);
+      compute(stage0, st);
+      if (st + 1 >= nst) break;
+      wait_dma();
+      __syncthreads();
+      if (st + 2 < nst) issue(stage0, st + 2);
+      compute(stage1, st + 1);
+    }
+    const float s = g.scale ? g.scale[a] : 1.0f;
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = t0 + 16 * wv + 4 * kg + j, rr = 16 * r + c;
+        if (t >= begin && t < end && rr < g.R32)
+          g.part[((int64_t)split * g.T + t) * g.R32 + rr] = rr < rank ? s * acc[r][j] : 0.0f;
+      }
+  });
 }
 
 // ------------------------------------------------------------------- gemm
@@ -362,45 +451,70 @@ struct ExpandArgs {
   int T, N, R, R32, splits;
 };
 
-// This lane's operand values u[t][k .. k+8), the splits added up, as P parts.
-template <int P>
-COLI_DEV void load_u(const ExpandArgs &g, int t, int k, bool live, uint4 (&uf)[P]) {
-  float v[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-  if (live) {
-    const float *p = g.u + (int64_t)t * g.R32 + k;
-#pragma unroll 4
-    for (int s = 0; s < g.splits; ++s) {
-      const float4 lo = *reinterpret_cast<const float4 *>(p + (int64_t)s * g.T * g.R32);
-      const float4 hi = *reinterpret_cast<const float4 *>(p + (int64_t)s * g.T * g.R32 + 4);
-      v[0] += lo.x;
-      v[1] += lo.y;
-      v[2] += lo.z;
-      v[3] += lo.w;
-      v[4] += hi.x;
-      v[5] += hi.y;
-      v[6] += hi.z;
-      v[7] += hi.w;
-    }
-  }
-  split8<P>(v, uf);
+// Sums of up to four parts, in order, at M places.  All loads of all places
+// are requested before any is used, and no more parts than there are.
+static_assert(kMaxSplits == 4, "sum_parts");
+COLI_DEV void add4(float4 &v, const float4 &o) {
+  v.x += o.x;
+  v.y += o.y;
+  v.z += o.z;
+  v.w += o.w;
 }
-// Ranks [k, k + 8) of the adapter's columns n0 + 4c + j.
-COLI_DEV void load_b(const ExpandArgs &g, int a, int n0, int k, int rank, uint4 (&bf)[4]) {
-  const int c = threadIdx.x & 15;
+template <int M>
+COLI_DEV void sum_parts(const float *const (&p)[M], int64_t stride, int splits, float4 (&v)[M]) {
+  auto load = [&](int s, float4 (&o)[M]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int n = min(n0 + 4 * c + j, g.N - 1);
-    bf[j] = k < rank ? keep_first(ld16(g.b + ((int64_t)a * g.N + n) * g.R + k), rank - k) : zero4();
+    for (int m = 0; m < M; ++m) o[m] = *reinterpret_cast<const float4 *>(p[m] + s * stride);
+  };
+  load(0, v);
+  if (splits == 1) return;
+  float4 a[M], b[M], c[M];
+  load(1, a);
+  if (splits > 2) {
+    load(2, b);
+    load(splits > 3 ? 3 : 2, c);
+  }
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    add4(v[m], a[m]);
+    if (splits > 2) add4(v[m], b[m]);
+    if (splits > 3) add4(v[m], c[m]);
   }
 }
 
-// acc += the adapters' part of the wavefront's MI x 4 tiles: rows t0 + 16i +
-// c, columns n0 + 4c + j.  Every request with rows here multiplies only the
+// This lane's operand values u[t][k .. k+8), the splits added up, as P parts;
+// zeros where not live.  Every lane loads (row t is in the batch, k in the
+// padded width): a branch around the loads would have each wait for the last.
+template <int P>
+COLI_DEV void load_u(const ExpandArgs &g, int t, int k, bool live, uint4 (&uf)[P]) {
+  const float *p = g.u + (int64_t)min(t, g.T - 1) * g.R32 + k;
+  const int64_t stride = (int64_t)g.T * g.R32;
+  const float *const at[2] = {p, p + 4};
+  float4 q[2];
+  sum_parts<2>(at, stride, g.splits, q);
+  float v[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = live ? v[e] : 0.0f;
+  split8<P>(v, uf);
+}
+// Ranks [k, k + 8) of the adapter's columns n0 + NJ c + j, zeros past its rank.
+template <int NJ>
+COLI_DEV void load_b(const ExpandArgs &g, int a, int n0, int k, int rank, uint4 (&bf)[NJ]) {
+  const int c = threadIdx.x & 15;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int n = min(n0 + NJ * c + j, g.N - 1);
+    bf[j] = ld16(g.b + ((int64_t)a * g.N + n) * g.R + min(k, g.R - 8));
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) bf[j] = keep_first(bf[j], rank - k);
+}
+
+// acc += the adapters' part of the wavefront's MI x NJ tiles: rows t0 + 16i +
+// c, columns n0 + NJ c + j.  Every request with rows here multiplies only the
 // 16-row tiles that it reaches, its other rows as zeros.
-template <int MI, int P>
-COLI_DEV void expand(const ExpandArgs &g, int t0, int n0, f32x4 (&acc)[MI][4]) {
+template <int MI, int NJ, int P>
+COLI_DEV void expand(const ExpandArgs &g, int t0, int n0, f32x4 (&acc)[MI][NJ]) {
   const int lane = threadIdx.x & 63, c = lane & 15, kg = lane >> 4;
   const int t1 = min(g.T, t0 + 16 * MI);
   if (t0 >= t1) return;
@@ -408,8 +522,8 @@ COLI_DEV void expand(const ExpandArgs &g, int t0, int n0, f32x4 (&acc)[MI][4]) {
     const int rank = rank_of(g.rank, a, g.R);
     for (int k0 = 0; k0 < rank; k0 += 32) {
       const int k = k0 + 8 * kg;  // this lane's eight ranks
-      uint4 bf[4];
-      load_b(g, a, n0, k, rank, bf);
+      uint4 bf[NJ];
+      load_b<NJ>(g, a, n0, k, rank, bf);
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
         if (begin >= t0 + 16 * i + 16 || end <= t0 + 16 * i) continue;
@@ -419,20 +533,43 @@ COLI_DEV void expand(const ExpandArgs &g, int t0, int n0, f32x4 (&acc)[MI][4]) {
 #pragma unroll
         for (int p = 0; p < P; ++p)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = mfma(uf[p], bf[j], acc[i][j]);
+          for (int j = 0; j < NJ; ++j) acc[i][j] = mfma(uf[p], bf[j], acc[i][j]);
       }
     }
   });
 }
 
-// Four neighbouring columns of one row.
-template <bool F32>
-COLI_DEV void store4(void *y, int64_t at, float a, float b, float c, float d) {
-  if (F32)
-    *reinterpret_cast<float4 *>(static_cast<float *>(y) + at) = make_float4(a, b, c, d);
-  else
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(y) + at) =
-        make_uint2(pack_bf16(a, b), pack_bf16(c, d));
+// NJ neighbouring columns of one row.
+template <int NJ, bool F32>
+COLI_DEV void store_cols(void *y, int64_t at, const float (&v)[NJ]) {
+  if (F32) {
+    float *p = static_cast<float *>(y) + at;
+    if (NJ == 4) *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[NJ > 1], v[NJ > 2 ? 2 : 0], v[NJ > 3 ? 3 : 0]);
+    else if (NJ == 2) *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[NJ > 1]);
+    else *p = v[0];
+  } else {
+    uint16_t *p = static_cast<uint16_t *>(y) + at;
+    if (NJ == 4)
+      *reinterpret_cast<uint2 *>(p) =
+          make_uint2(pack_bf16(v[0], v[NJ > 1]), pack_bf16(v[NJ > 2 ? 2 : 0], v[NJ > 3 ? 3 : 0]));
+    else if (NJ == 2) *reinterpret_cast<uint32_t *>(p) = pack_bf16(v[0], v[NJ > 1]);
+    else *p = (uint16_t)pack_bf16(v[0], 0.0f);
+  }
+}
+template <int MI, int NJ, bool F32>
+COLI_DEV void store_tile(void *y, int T, int N, int t0, int n0, const f32x4 (&acc)[MI][NJ]) {
+  const int c = threadIdx.x & 15, kg = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int t = t0 + 16 * i + 4 * kg + e;
+      if (t >= T) continue;
+      float v[NJ];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) v[j] = acc[i][j][e];
+      store_cols<NJ, F32>(y, (int64_t)t * N + n0 + NJ * c, v);
+    }
 }
 
 struct GemmArgs {
@@ -445,89 +582,189 @@ struct GemmArgs {
 };
 
 // BM x BN tile, wavefronts of WM x 64.  Stages of 64 k go global -> LDS by
-// DMA, two in turn.  A row's 16-byte chunk q is kept at q ^ (row & 7) for x
-// and at q ^ ((row >> 2) & 7) for w, whose rows are read in the order
-// n = 4c + j: lane c then ends up with four neighbouring columns, stored
-// together, and neither operand read meets a bank conflict.
+// DMA, two buffers in turn, and from there to registers one stage ahead:
+// while a stage is multiplied, the next one's operands are read from LDS and
+// the one after it is copied into the buffer that was emptied a stage ago.
+//
+// Lane (c, g) of a 16 x 16 x 32 step h holds k = 32h + 8g of row c: chunk g +
+// 4h of the row's eight 16-byte chunks, kept at (g + 4h) ^ (row & 7).  LDS
+// serves the chunks of lanes g and g + 1 of eight rows together, which then
+// fall on distinct banks (with chunks 2g + h, two apart, they collide: the
+// reads took 1.5 times as long).  w's rows are kept in the order n = 4c + j,
+// so that lane c ends up with four neighbouring columns, stored together.
 template <int BM, int BN, int WM, bool SCALED, bool F32>
-__global__ void __launch_bounds__(BM / WM *BN / 64 * 64) gemm_kernel(GemmArgs g) {
+__global__ void __launch_bounds__(BM / WM * BN) gemm_kernel(GemmArgs g) {
   constexpr int NW = (BM / WM) * (BN / 64), MI = WM / 16;
   constexpr int LD = (BM + BN) / 8 / NW;  // DMA instructions of a wavefront per stage
-  __shared__ uint4 lds[2][(BM + BN) * 8];
+  constexpr int VM = LD + (SCALED ? 1 : 0);
+  // three objects, so that the compiler sees that one is read while others fill
+  __shared__ uint4 stage0[(BM + BN) * 8], stage1[(BM + BN) * 8], stage2[(BM + BN) * 8];
   const int lane = threadIdx.x & 63, c = lane & 15, kg = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tm = blockIdx.y * BM, tn = blockIdx.x * BN;
+  // Workgroups go to the 8 XCDs in turn; each XCD gets a run of neighbouring
+  // tiles (all columns of a few row tiles), so that its L2 holds those rows
+  // of x once instead of every row.
+  const int cols_t = (g.N + BN - 1) / BN;
+  const int tile = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+  const int tm = tile / cols_t * BM, tn = tile % cols_t * BN;
+  if (tm >= g.T) return;
   const int wm = (wv / (BN / 64)) * WM, wn = (wv % (BN / 64)) * 64;
 
-  const uint16_t *src[LD];
+  uint32_t src[LD];  // byte offsets: a matrix has at most 2^31 bytes
 #pragma unroll
   for (int i = 0; i < LD; ++i) {
     const int row = (wv * LD + i) * 8 + (lane >> 3), pos = lane & 7;
-    if (row < BM) {
-      src[i] = g.x + (int64_t)min(tm + row, g.T - 1) * g.K + 8 * (pos ^ (row & 7));
+    if ((wv * LD + i) * 8 < BM) {
+      src[i] = (uint32_t)min(tm + row, g.T - 1) * (uint32_t)g.K * 2u + 16u * (pos ^ (row & 7));
     } else {
-      const int r = row - BM;
-      src[i] = g.w + (int64_t)min(tn + r, g.N - 1) * g.K + 8 * (pos ^ ((r >> 2) & 7));
+      const int r = row - BM, n = (r & ~63) + 4 * (r & 15) + ((r >> 4) & 3);
+      src[i] = (uint32_t)min(tn + n, g.N - 1) * (uint32_t)g.K * 2u + 16u * (pos ^ (r & 7));
     }
   }
-  auto issue = [&](int st) {
+  const int n0 = tn + wn;
+  const float *scp = g.sc + min(n0, g.N - 64) + 4 * c;  // N is a multiple of 64
+  const int nst = g.K / 64;
+  // past the last stage the copies repeat it, so that every stage leaves the
+  // same number of operations in flight
+  auto issue_one = [&](uint4 *to, int st, int i) {
+    const char *base = reinterpret_cast<const char *>((wv * LD + i) * 8 < BM ? g.x : g.w);
+    dma16(base + 128 * min(st, nst - 1) + src[i], to + (wv * LD + i) * 64);
+  };
+  auto issue = [&](uint4 *to, int st) {
 #pragma unroll
-    for (int i = 0; i < LD; ++i) dma16(src[i] + 64 * st, &lds[st & 1][(wv * LD + i) * 64]);
+    for (int i = 0; i < LD; ++i) issue_one(to, st, i);
   };
   f32x4 acc[MI][4];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  const int n0 = tn + wn;
-  const bool cols = n0 < g.N;  // N is a multiple of 64
-  const float *scp = g.sc + n0 + 4 * c;
-  const int nst = g.K / 64;
-  issue(0);
-  for (int st = 0; st < nst; ++st) {
-    float4 s4 = make_float4(1, 1, 1, 1);
-    if (SCALED && cols) s4 = *reinterpret_cast<const float4 *>(scp + (int64_t)st * g.N);
-    wait_dma();
-    __syncthreads();
-    if (st + 1 < nst) issue(st + 1);
-    const uint4 *A = lds[st & 1], *B = A + BM * 8;
-    uint4 bf[4][2];
+  // with scales: a row tile's partial products join the sums (plain floats,
+  // which the compiler keeps in place) while the matrix cores work on the
+  // next row tile's
+  float sums[MI][4][4];
+  f32x4 dprev[4];
+  float4 sprev = make_float4(0, 0, 0, 0), s0 = sprev, s1 = sprev, s2 = sprev;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < 4; ++j) dprev[j] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        bf[j][h] = B[(wn + 4 * c + j) * 8 + ((2 * kg + h) ^ (c & 7))];
+  for (int i = 0; i < MI * 16; ++i) (&sums[0][0][0])[i] = 0.0f;
+  auto add_scaled = [&](float (&to)[4][4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float s = j == 0 ? sprev.x : (j == 1 ? sprev.y : (j == 2 ? sprev.z : sprev.w));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) to[j][e] = fmaf(dprev[j][e], s, to[j][e]);
+    }
+  };
+  // with scales there are registers for one set of w's operands: the last row
+  // tile reads each one's successor as soon as it has used it
+  uint4 af[MI][2], bf[SCALED ? 1 : 2][4][2];
+  auto read_a = [&](const uint4 *A, int i) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) af[i][h] = A[(wm + 16 * i + c) * 8 + ((kg + 4 * h) ^ (c & 7))];
+  };
+  auto read_b = [&](const uint4 *A, int j, uint4 (&to)[4][2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) to[j][h] = A[(BM + wn + 16 * j + c) * 8 + ((kg + 4 * h) ^ (c & 7))];
+  };
+  // Stage st: its operands are in af and b; `next` holds the next stage, the
+  // one after that is on its way, and `to` (this stage's buffer, emptied)
+  // takes the third.
+  // Its scales are in s4; those of stage st + 2 are loaded into s6.
+  auto compute = [&](uint4 (&b)[4][2], uint4 (&bnext)[4][2], const uint4 *next, uint4 *to,
+                     const float4 &s4, float4 &s6, int st) {
+    // the next stage is there, this one's reads are done
+    __builtin_amdgcn_s_waitcnt(0x0070 | (VM & 15));
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (SCALED) s6 = *reinterpret_cast<const float4 *>(scp + (int64_t)min(st + 2, nst - 1) * g.N);
+    __builtin_amdgcn_sched_barrier(0);
+    // the copies are spread over the stage: issued in one go, they would hold
+    // up every wavefront's start while the memory pipeline takes them in
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      uint4 af[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) af[h] = A[(wm + 16 * i + c) * 8 + ((2 * kg + h) ^ (c & 7))];
+      for (int q = i * LD / MI; q < (i + 1) * LD / MI; ++q) issue_one(to, st + 3, q);
+      if (SCALED) {
+        f32x4 d[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (SCALED) {
-          f32x4 d = mfma(af[0], bf[j][0], f32x4{0, 0, 0, 0});
-          d = mfma(af[1], bf[j][1], d);
-          const float s = j == 0 ? s4.x : (j == 1 ? s4.y : (j == 2 ? s4.z : s4.w));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[e], s, acc[i][j][e]);
-        } else {
-          acc[i][j] = mfma(af[0], bf[j][0], acc[i][j]);
-          acc[i][j] = mfma(af[1], bf[j][1], acc[i][j]);
+        for (int j = 0; j < 4; ++j) {
+          d[j] = mfma(af[i][0], b[j][0], f32x4{0, 0, 0, 0});
+          d[j] = mfma(af[i][1], b[j][1], d[j]);
+          if (i == MI - 1) read_b(next, j, b);
         }
+        add_scaled(sums[(i + MI - 1) % MI]);
+        if (i == 0) sprev = s4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dprev[j] = d[j];
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = mfma(af[i][h], b[j][h], acc[i][j]);
+      }
+      // past the last stage this reads what is there, unused
+      read_a(next, i);
+      if (!SCALED) {
+#pragma unroll
+        for (int j = 4 * i / MI; j < 4 * (i + 1) / MI; ++j) read_b(next, j, bnext);
+      }
+      if (SCALED) {
+        __builtin_amdgcn_sched_barrier(0);
+        continue;
+      }
+      constexpr int R = 2 + 8 / MI;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        if (q * R / 8 != (q + 1) * R / 8) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        if (q == 2 || q == 6) __builtin_amdgcn_sched_group_barrier(0x10, 1, 0);
       }
     }
+  };
+  issue(stage0, 0);
+  if (SCALED) {
+    s0 = *reinterpret_cast<const float4 *>(scp);
+    s1 = *reinterpret_cast<const float4 *>(scp + (int64_t)min(1, nst - 1) * g.N);
   }
-  if (!cols) return;
-  if (g.e.u) expand<MI, F32 ? 3 : 2>(g.e, tm + wm, n0, acc);
+  issue(stage1, 1);
+  issue(stage2, 2);
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (2 * LD & 15) | (2 * LD >> 4 << 14));
+  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < MI; ++i)
+  for (int i = 0; i < MI; ++i) read_a(stage0, i);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int t = tm + wm + 16 * i + 4 * kg + e;
-      if (t < g.T)
-        store4<F32>(g.y, (int64_t)t * g.N + n0 + 4 * c, acc[i][0][e], acc[i][1][e], acc[i][2][e],
-                    acc[i][3][e]);
-    }
+  for (int j = 0; j < 4; ++j) read_b(stage0, j, bf[0]);
+  constexpr int B1 = SCALED ? 0 : 1;
+  int st = 0;
+  for (; st + 6 <= nst; st += 6) {
+    compute(bf[0], bf[B1], stage1, stage0, s0, s2, st);
+    compute(bf[B1], bf[0], stage2, stage1, s1, s0, st + 1);
+    compute(bf[0], bf[B1], stage0, stage2, s2, s1, st + 2);
+    compute(bf[B1], bf[0], stage1, stage0, s0, s2, st + 3);
+    compute(bf[0], bf[B1], stage2, stage1, s1, s0, st + 4);
+    compute(bf[B1], bf[0], stage0, stage2, s2, s1, st + 5);
+  }
+  if (st < nst) compute(bf[0], bf[B1], stage1, stage0, s0, s2, st);
+  if (st + 1 < nst) compute(bf[B1], bf[0], stage2, stage1, s1, s0, st + 1);
+  if (st + 2 < nst) compute(bf[0], bf[B1], stage0, stage2, s2, s1, st + 2);
+  if (st + 3 < nst) compute(bf[B1], bf[0], stage1, stage0, s0, s2, st + 3);
+  if (st + 4 < nst) compute(bf[0], bf[B1], stage2, stage1, s1, s0, st + 4);
+  wait_dma();  // nothing may land in LDS after the workgroup has ended
+  if (SCALED) {
+    add_scaled(sums[MI - 1]);
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = sums[i][j][e];
+  }
+  if (n0 >= g.N) return;
+  if (g.e.u) expand<MI, 4, F32 ? 3 : 2>(g.e, tm + wm, n0, acc);
+  store_tile<MI, 4, F32>(g.y, g.T, g.N, tm + wm, n0, acc);
 }
 
 // ----------------------------------------------------------------- stream
@@ -543,7 +780,7 @@ struct StreamArgs {
   float *part;        // [splits][T][N]
   int T, splits, per;  // per: 64-wide groups of a wavefront
   int shrink_blocks, shrink_tiles;
-  ShrinkArgs s;
+  ShrinkArgs s[2];  // u, and in the backward pass v
 };
 
 constexpr int kStreamWaves = 8;
@@ -552,18 +789,22 @@ constexpr int kStreamWaves = 8;
 // the group, g = lane / 16), in two steps of eight.
 template <int F>
 struct Raw {
-  uint32_t w[F == kI8 ? 4 : 2];
+  uint32_t w[F == kBF ? 8 : (F == kI8 ? 4 : 2)];
   uint32_t s;
 };
 template <int F>
 COLI_DEV Raw<F> load_raw(const Matrix &m, int n, int b, int kg) {
   Raw<F> r;
+  if (F == kBF) {
+    const uint16_t *p = reinterpret_cast<const uint16_t *>(m.q) + (int64_t)n * m.K + 64 * b + 16 * kg;
+    const uint4 v[2] = {ld16(p), ld16(p + 8)};
+    __builtin_memcpy(r.w, v, sizeof(r.w));
+    r.s = 0;
+    return r;
+  }
   if (F == kI8) {
     const uint4 v = ld16(m.q + (int64_t)n * m.K + 64 * b + 16 * kg);
-    r.w[F == kI8 ? 2 : 0] = v.z;
-    r.w[F == kI8 ? 3 : 0] = v.w;
-    r.w[0] = v.x;
-    r.w[1] = v.y;
+    __builtin_memcpy(r.w, &v, F == kI8 ? 16 : 8);
   } else {
     const uint2 v = *reinterpret_cast<const uint2 *>(m.q + ((int64_t)n * m.K + 64 * b + 16 * kg) / 2);
     r.w[0] = v.x;
@@ -579,6 +820,11 @@ COLI_DEV Raw<F> load_raw(const Matrix &m, int n, int b, int kg) {
 // values.  MXFP4: the weights themselves.
 template <int F>
 COLI_DEV uint4 unpack(const Raw<F> &r, int h) {
+  if (F == kBF) {
+    uint4 v;
+    __builtin_memcpy(&v, &r.w[F == kBF ? 4 * h : 0], F == kBF ? 16 : 8);
+    return v;
+  }
   if (F == kI4) {
     const uint32_t w = r.w[h];
     constexpr uint32_t M = 0x00780078u, X = 0x41c041c0u;
@@ -620,6 +866,7 @@ COLI_DEV void stream_tile(const StreamArgs &g, int nt, int tt, int split, f32x4 
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  constexpr bool exact = F == kF4 || F == kBF;  // operands are whole weights
   const uint16_t *xrow = g.x + (int64_t)(t0 + c) * g.m.K + 16 * kg;
   for (int b = b0; b < b1; b += GB) {
     Raw<F> raw[GB][NJ];
@@ -660,13 +907,13 @@ COLI_DEV void stream_tile(const StreamArgs &g, int nt, int tt, int split, f32x4 
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         const uint4 w0 = unpack<F>(raw[i][j], 0), w1 = unpack<F>(raw[i][j], 1);
-        const float s = F == kF4 ? 1.0f : f16_to_f32((uint16_t)raw[i][j].s);
+        const float s = exact ? 1.0f : f16_to_f32((uint16_t)raw[i][j].s);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          f32x4 d = F == kF4 ? acc[m][j] : start[m];
+          f32x4 d = exact ? acc[m][j] : start[m];
           d = mfma(xr[i][m][0], w0, d);
           d = mfma(xr[i][m][1], w1, d);
-          if (F == kF4) {
+          if (exact) {
             acc[m][j] = d;
           } else {
 #pragma unroll
@@ -685,7 +932,9 @@ COLI_DEV void stream_tile(const StreamArgs &g, int nt, int tt, int split, f32x4 
       const int t = t0 + 16 * m + 4 * kg + e;
       if (t >= g.T) continue;
       float *p = g.part + ((int64_t)split * g.T + t) * g.m.N + n0 + NJ * c;
-      if (NJ == 4) {
+      if (NJ == 2) {
+        *reinterpret_cast<float2 *>(p) = make_float2(acc[m][0][e], acc[m][NJ > 1][e]);
+      } else if (NJ == 4) {
         *reinterpret_cast<float4 *>(p) =
             make_float4(acc[m][0][e], acc[m][NJ > 1][e], acc[m][NJ > 2 ? 2 : 0][e], acc[m][NJ > 3 ? 3 : 0][e]);
       } else {
@@ -695,15 +944,23 @@ COLI_DEV void stream_tile(const StreamArgs &g, int nt, int tt, int split, f32x4 
     }
 }
 
+// Workgroup b of the u (and v) side.
+template <int RT, int NW>
+COLI_DEV void shrink_block(const StreamArgs &g, int b, f32x4 (*buf)[64]) {
+  const int tile = b % g.shrink_tiles;
+  b /= g.shrink_tiles;
+  const int sub = b % g.s[0].nsub, split = b / g.s[0].nsub;
+  if (split < g.s[0].splits) shrink_tile<RT, 1, NW>(g.s[0], tile, sub, split, buf);
+  else shrink_tile<RT, 1, NW>(g.s[1], tile, sub, split - g.s[0].splits, buf);
+}
+
 template <int F, int MT, int NJ, int GB, int RT>
 __global__ void __launch_bounds__(64 * kStreamWaves) stream_kernel(StreamArgs g) {
   constexpr int A = MT * NJ > RT ? MT * NJ : RT;
   __shared__ f32x4 buf[kStreamWaves / 2 * A][64];
   int b = blockIdx.x;
   if (b < g.shrink_blocks) {
-    const int tile = b % g.shrink_tiles;
-    b /= g.shrink_tiles;
-    shrink_tile<RT, 1, kStreamWaves>(g.s, tile, b % g.s.nsub, b / g.s.nsub, buf);
+    shrink_block<RT, kStreamWaves>(g, b, buf);
     return;
   }
   b -= g.shrink_blocks;
@@ -711,6 +968,139 @@ __global__ void __launch_bounds__(64 * kStreamWaves) stream_kernel(StreamArgs g)
   const int n = b % nt;
   b /= nt;
   stream_tile<F, MT, NJ, GB>(g, n, b % tt, b / tt, buf);
+}
+
+// ----------------------------------------------------------------- direct
+//
+// The codes again go from memory straight into registers, but x is staged in
+// LDS (two 64-wide groups per stage, two stages in turn) and shared by the
+// workgroup's four wavefronts, 64 rows x 32 columns each.  Otherwise as the
+// streaming path: parts and u first, joined by the second launch.
+constexpr int kDirectM = 4, kDirectN = 2, kDirectWaves = 4, kDirectGroups = 2;
+constexpr int kDirectRows = 16 * kDirectM, kDirectCols = 16 * kDirectN * kDirectWaves;
+
+template <int F>
+COLI_DEV void direct_tile(const StreamArgs &g, int nt, int tt, int split, uint4 *stage0,
+                          uint4 *stage1) {
+  constexpr int MT = kDirectM, NJ = kDirectN, NW = kDirectWaves, KS = kDirectGroups;
+  constexpr int RB = 8 * KS;                      // 16-byte chunks of a staged row
+  constexpr int LD = kDirectRows * RB / 64 / NW;  // DMA instructions of a wavefront per stage
+  constexpr bool exact = F == kF4 || F == kBF;
+  const int lane = threadIdx.x & 63, c = lane & 15, kg = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tm = tt * kDirectRows, n0 = nt * kDirectCols + wv * (16 * NJ);
+  const int ns = min(n0, g.m.N - 16 * NJ);  // wavefronts past the last column read that one's
+  const int g0 = split * g.per, g1 = min(g.m.K / 64, g0 + g.per);  // groups of this split
+  const int nst = (g1 - g0 + KS - 1) / KS;
+  // Chunk p of row r is kept at p ^ key(r): LDS serves eight rows' chunks of
+  // lanes kg and kg + 1 together, which are two apart.
+  auto key = [](int r) {
+    return KS == 1 ? ((r >> 1) & 1) | ((r >> 2) & 1) << 2 : (r & 1) | ((r >> 1) & 3) << 2;
+  };
+  static_assert(KS <= 2, "keys for rows of 8 and 16 chunks");
+  const uint16_t *src[LD];
+#pragma unroll
+  for (int i = 0; i < LD; ++i) {
+    const int q = (wv * LD + i) * 64 + lane, row = q / RB, pos = q % RB;
+    src[i] = g.x + (int64_t)min(tm + row, g.T - 1) * g.m.K + 64 * g0 + 8 * (pos ^ key(row));
+  }
+  const int nb = g1 - g0;
+  Raw<F> raw[KS][NJ];
+  auto issue = [&](uint4 *to, int st) {
+#pragma unroll
+    for (int i = 0; i < LD; ++i) {
+      // the last stage may be short: its missing groups are not used
+      const int q = (wv * LD + i) * 64 + lane, pos = (q % RB) ^ key(q / RB);
+      const int over = KS > 1 ? max(0, 64 * (KS * st + pos / 8 - nb + 1)) : 0;
+      dma16(src[i] + 64 * KS * st - over, to + (wv * LD + i) * 64);
+    }
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        raw[s][j] = load_raw<F>(g.m, ns + NJ * c + j, g0 + min(KS * st + s, nb - 1), kg);
+  };
+  f32x4 acc[MT][NJ];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  auto compute = [&](const uint4 *A, uint4 *to, int st) {
+    uint4 w[KS][NJ][2];
+    float sc[KS][NJ];
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        w[s][j][0] = unpack<F>(raw[s][j], 0);
+        w[s][j][1] = unpack<F>(raw[s][j], 1);
+        sc[s][j] = exact ? 1.0f : f16_to_f32((uint16_t)raw[s][j].s);
+      }
+    if (st + 1 < nst) issue(to, st + 1);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      if (KS > 1 && KS * st + s >= nb) continue;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        uint4 af[2];
+        f32x4 start = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          af[h] = A[(16 * i + c) * RB + ((8 * s + 2 * kg + h) ^ key(c))];
+          if (F == kI4) {
+            constexpr uint32_t kMinus24 = 0xc1c0c1c0u;
+            const uint32_t d[4] = {af[h].x, af[h].y, af[h].z, af[h].w};
+            uint32_t o[4];
+            x8_to_pairs(d, o);
+            af[h] = make_uint4(o[0], o[1], o[2], o[3]);
+            start = mfma(af[h], make_uint4(kMinus24, kMinus24, kMinus24, kMinus24), start);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          f32x4 d = exact ? acc[i][j] : start;
+          d = mfma(af[0], w[s][j][0], d);
+          d = mfma(af[1], w[s][j][1], d);
+          if (exact) {
+            acc[i][j] = d;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[e], sc[s][j], acc[i][j][e]);
+          }
+        }
+      }
+    }
+  };
+  if (nb > 0) {
+    issue(stage0, 0);
+    for (int st = 0; st < nst; st += 2) {
+      wait_dma();
+      __syncthreads();
+      compute(stage0, stage1, st);
+      if (st + 1 == nst) break;
+      wait_dma();
+      __syncthreads();
+      compute(stage1, stage0, st + 1);
+    }
+  }
+  if (n0 >= g.m.N) return;
+  store_tile<MT, NJ, true>(g.part + (int64_t)split * g.T * g.m.N, g.T, g.m.N, tm, n0, acc);
+}
+
+template <int F, int RT>
+__global__ void __launch_bounds__(64 * kDirectWaves) direct_kernel(StreamArgs g) {
+  __shared__ uint4 stage0[kDirectRows * 8 * kDirectGroups], stage1[kDirectRows * 8 * kDirectGroups];
+  __shared__ f32x4 buf[kDirectWaves / 2 * RT][64];
+  int b = blockIdx.x;
+  if (b < g.shrink_blocks) {
+    shrink_block<RT, kDirectWaves>(g, b, buf);
+    return;
+  }
+  b -= g.shrink_blocks;
+  const int nt = (g.m.N + kDirectCols - 1) / kDirectCols, tt = (g.T + kDirectRows - 1) / kDirectRows;
+  const int n = b % nt;
+  b /= nt;
+  direct_tile<F>(g, n, b % tt, b / tt, stage0, stage1);
 }
 
 // y = the sum of the parts, plus the adapters.  A wavefront takes 64 columns
@@ -724,34 +1114,29 @@ struct CombineArgs {
   ExpandArgs e;
 };
 template <bool F32>
-__global__ void __launch_bounds__(256) combine_parts_kernel(CombineArgs g) {
+COLI_DEV void combine_tile(const CombineArgs &g, int nx, int ty, int sub) {
   const int lane = threadIdx.x & 63, c = lane & 15, kg = lane >> 4;
-  const int n0 = (blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * 64;
+  const int n0 = (nx * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * 64;
   if (n0 >= g.e.N) return;
-  const int t0 = blockIdx.y * 16, t1 = min(g.e.T, t0 + 16), sub = blockIdx.z;
+  const int t0 = ty * 16, t1 = min(g.e.T, t0 + 16);
   uint32_t covered = 0;
   auto rows = [&](int begin, int end, uint32_t mask, int a) {
-    f32x4 acc[4];
+    // the four rows of this lane, if any of them is wanted
+    f32x4 acc[4] = {};
+    if ((mask >> (4 * kg)) & 15u) {
+      const float *at[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int r = 4 * kg + e;
-      const bool mine = (mask >> r) & 1u;
-      float4 v = make_float4(0, 0, 0, 0);
-      if (mine) {
-        const float *p = g.part + (int64_t)(t0 + r) * g.e.N + n0 + 4 * c;
-#pragma unroll 4
-        for (int s = 0; s < g.splits; ++s) {
-          const float4 o = *reinterpret_cast<const float4 *>(p + (int64_t)s * g.e.T * g.e.N);
-          v.x += o.x;
-          v.y += o.y;
-          v.z += o.z;
-          v.w += o.w;
-        }
+      for (int e = 0; e < 4; ++e)
+        at[e] = g.part + (int64_t)min(t0 + 4 * kg + e, g.e.T - 1) * g.e.N + n0 + 4 * c;
+      float4 v[4];
+      sum_parts<4>(at, (int64_t)g.e.T * g.e.N, g.splits, v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[0][e] = v[e].x;
+        acc[1][e] = v[e].y;
+        acc[2][e] = v[e].z;
+        acc[3][e] = v[e].w;
       }
-      acc[0][e] = v.x;
-      acc[1][e] = v.y;
-      acc[2][e] = v.z;
-      acc[3][e] = v.w;
     }
     if (a >= 0) {
       constexpr int P = F32 ? 3 : 2;
@@ -760,7 +1145,7 @@ __global__ void __launch_bounds__(256) combine_parts_kernel(CombineArgs g) {
       for (int k0 = 0; k0 < rank; k0 += 32) {
         const int k = k0 + 8 * kg;
         uint4 bf[4], uf[P];
-        load_b(g.e, a, n0, k, rank, bf);
+        load_b<4>(g.e, a, n0, k, rank, bf);
         load_u<P>(g.e, t, k, t >= begin && t < end && k < rank, uf);
 #pragma unroll
         for (int p = 0; p < P; ++p)
@@ -771,9 +1156,10 @@ __global__ void __launch_bounds__(256) combine_parts_kernel(CombineArgs g) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int r = 4 * kg + e;
-      if ((mask >> r) & 1u)
-        store4<F32>(g.y, (int64_t)(t0 + r) * g.e.N + n0 + 4 * c, acc[0][e], acc[1][e], acc[2][e],
-                    acc[3][e]);
+      if ((mask >> r) & 1u) {
+        const float v[4] = {acc[0][e], acc[1][e], acc[2][e], acc[3][e]};
+        store_cols<4, F32>(g.y, (int64_t)(t0 + r) * g.e.N + n0 + 4 * c, v);
+      }
     }
   };
   if (g.e.u) {
@@ -785,6 +1171,11 @@ __global__ void __launch_bounds__(256) combine_parts_kernel(CombineArgs g) {
   }
   const uint32_t rest = ((1u << (t1 - t0)) - 1u) & ~covered;
   if (sub == 0 && rest) rows(0, 0, rest, -1);
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(256) combine_parts_kernel(CombineArgs g) {
+  combine_tile<F32>(g, blockIdx.x, blockIdx.y, blockIdx.z);
 }
 
 // ----------------------------------------------------------------- finish
@@ -801,10 +1192,10 @@ struct FinishArgs {
   int32_t *owner;        // [Tp]
   int T, Tp, R32;
 };
-__global__ void __launch_bounds__(256) finish_kernel(FinishArgs g) {
+COLI_DEV void finish_tile(const FinishArgs &g, int tile, int rank_block, int w) {
   __shared__ float s[64][33];
   __shared__ int own[64];
-  const int tid = threadIdx.x, t0 = blockIdx.x * 64, r0 = blockIdx.y * 32, w = blockIdx.z;
+  const int tid = threadIdx.x, t0 = tile * 64, r0 = rank_block * 32;
   if (tid < 64) {
     const int t = t0 + tid;
     int a = -1;
@@ -822,14 +1213,17 @@ __global__ void __launch_bounds__(256) finish_kernel(FinishArgs g) {
     if (w == 0 && r0 == 0) g.owner[t] = a;
   }
   __syncthreads();
+#pragma unroll 2
   for (int i = tid; i < 64 * 32; i += 256) {
     const int tt = i >> 5, r = i & 31;
     float v = 0.0f;
     if (own[tt] >= 0) {
       const float *p = g.part[w] + (int64_t)(t0 + tt) * g.R32 + r0 + r;
-      for (int k = 0; k < g.splits[w]; ++k) v += p[(int64_t)k * g.T * g.R32];
+#pragma unroll
+      for (int k = 0; k < kMaxSplits; ++k)
+        if (k < g.splits[w]) v += p[(int64_t)k * g.T * g.R32];
     }
-    if (w == 1 && t0 + tt < g.T) g.rows[(int64_t)(t0 + tt) * g.R32 + r0 + r] = v;
+    if (g.rows && w == 1 && t0 + tt < g.T) g.rows[(int64_t)(t0 + tt) * g.R32 + r0 + r] = v;
     s[tt][r] = v;
   }
   __syncthreads();
@@ -842,6 +1236,24 @@ __global__ void __launch_bounds__(256) finish_kernel(FinishArgs g) {
 #pragma unroll
   for (int p = 0; p < 3; ++p)
     *reinterpret_cast<uint4 *>(g.planes[w] + ((int64_t)p * g.R32 + r0 + r) * g.Tp + t0 + tt) = parts[p];
+}
+
+__global__ void __launch_bounds__(256) finish_kernel(FinishArgs g) {
+  finish_tile(g, blockIdx.x, blockIdx.y, blockIdx.z);
+}
+
+// The backward pass's third launch for short batches: dx from its parts, and
+// finish.
+__global__ void __launch_bounds__(256) combine_finish_kernel(CombineArgs c, FinishArgs f,
+                                                             int combine_blocks) {
+  int b = blockIdx.x;
+  if (b < combine_blocks) {
+    const int nx = (c.e.N + 255) / 256, ny = (c.e.T + 15) / 16;
+    combine_tile<false>(c, b % nx, b / nx % ny, b / nx / ny);
+    return;
+  }
+  b -= combine_blocks;
+  finish_tile(f, b % (f.Tp / 64), b / (f.Tp / 64) % (f.R32 / 32), b / (f.Tp / 64) / (f.R32 / 32));
 }
 
 // ------------------------------------------------------------------ grads
@@ -873,7 +1285,12 @@ __global__ void __launch_bounds__(256) grads_kernel(GradsArgs a) {
   const int lane = threadIdx.x & 63, c = lane & 15, kg = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool second = (int)blockIdx.x >= a.g[0].f_tiles;
-  const GradArgs &g = a.g[second];
+  GradArgs g = a.g[0];  // field by field, as in pick()
+  g.z = second ? a.g[1].z : g.z;
+  g.planes = second ? a.g[1].planes : g.planes;
+  g.out = second ? a.g[1].out : g.out;
+  g.F = second ? a.g[1].F : g.F;
+  g.transposed = second ? a.g[1].transposed : g.transposed;
   const int f0 = ((int)blockIdx.x - (second ? a.g[0].f_tiles : 0)) * 128 + 8 * c;
   const int ad = blockIdx.y;
   const int split = blockIdx.z % a.splits, r0 = blockIdx.z / a.splits * (16 * RT);
@@ -966,18 +1383,21 @@ struct ReduceArgs {
 };
 __global__ void __launch_bounds__(256) reduce_kernel(ReduceArgs a) {
   int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int w = i >= a.n[0];
-  if (w) i -= a.n[0];
-  if (i >= a.n[w]) return;
-  float4 v = a.src[w][i];
+  const bool second = i >= a.n[0];
+  if (second) i -= a.n[0];
+  const int64_t n = second ? a.n[1] : a.n[0];
+  if (i >= n) return;
+  const float4 *src = second ? a.src[1] : a.src[0];
+  float4 v = src[i];
+#pragma unroll 4
   for (int s = 1; s < a.splits; ++s) {
-    const float4 o = a.src[w][s * a.n[w] + i];
+    const float4 o = src[s * n + i];
     v.x += o.x;
     v.y += o.y;
     v.z += o.z;
     v.w += o.w;
   }
-  a.dst[w][i] = v;
+  (second ? a.dst[1] : a.dst[0])[i] = v;
 }
 
 // ----------------------------------------------------------------- launch
@@ -998,9 +1418,9 @@ int round32(int r) { return (r + 31) / 32 * 32; }
 // 256 values each.
 int shrink_splits(int T, int F) {
   const int tiles = (T + 63) / 64;
-  int s = 512 / tiles;
+  int s = 256 / tiles;
   if (s > F / 256) s = F / 256;
-  return s < 1 ? 1 : (s > 8 ? 8 : s);
+  return s < 1 ? 1 : (s > kMaxSplits ? kMaxSplits : s);
 }
 // Row ranges of the gradients: about 1,024 workgroups.
 int grad_splits(int T, int N, int K, int n) {
@@ -1011,26 +1431,46 @@ int grad_splits(int T, int N, int K, int n) {
   return (int)(s > 16 ? 16 : s);
 }
 
-// Batches of up to this many rows take the streaming path.
-constexpr int kStreamRows = 640;
+// Which kernels compute T x K times N x K.  Measured on int4 (us, stream /
+// direct / gemm, each with the launches it needs):
+//   N 2048 K 6144, T  64: 21 / 25 / 85   T 256: 33 / 28 / 82   T 1024: 102 / 70 / 77
+//   N 6144 K 2048, T  64: 18 / 15 / 44   T 256: 42 / 29 / 43   T 1024: 118 / 68 / 41
+//   N 2048 K 1024, T  64: 13 / 10 / 19   T 517: 25 / 20 / 21   T 2048: the gemm
+// The streaming kernel reads x once per 16-64 columns, which pays only for
+// few rows (more of them where K is long and its splits keep the chip busy);
+// the gemm needs its 256 x 128 tiles to reach most CUs and a pass that
+// unpacks the weights.
+enum Path { kStream, kDirect, kGemm };
+Path path_of(int T, int N, int K) {
+  if (T <= (K > 4096 ? 128 : 32)) return kStream;
+  const int tiles = (T + 255) / 256 * ((N + 127) / 128);
+  return T > 512 && tiles >= 96 ? kGemm : kDirect;
+}
 // The streaming path's tiles: columns per workgroup grow with the rows, so
 // that x is not read once per 16 columns.
 int stream_mt(int T) { return T <= 16 ? 1 : (T <= 32 ? 2 : 4); }
-int stream_splits(int T, int N, int K) {
+int clamp_splits(int s, int most) {
+  if (s > most) s = most;
+  return s < 1 ? 1 : (s > kMaxSplits ? kMaxSplits : s);
+}
+int part_splits(int T, int N, int K) {
+  if (path_of(T, N, K) == kDirect) {
+    const int tiles = (N + kDirectCols - 1) / kDirectCols * ((T + kDirectRows - 1) / kDirectRows);
+    return clamp_splits(512 / tiles, K / 64 / (2 * kDirectGroups));
+  }
   const int mt = stream_mt(T);
   const int blocks = N / (16 * mt) * ((T + 16 * mt - 1) / (16 * mt));
-  int s = 384 / blocks;
-  const int most = K / 64 / kStreamWaves;
-  if (s > most) s = most;
-  return s < 1 ? 1 : (s > 8 ? 8 : s);
+  return clamp_splits(256 / blocks, K / 64 / kStreamWaves);
 }
-
-int stream_shrink_splits(int T, int F) {
-  // a run of 64-wide blocks per wavefront
-  int s = 64 / ((T + 15) / 16);
-  const int most = (F / 64 + kStreamWaves - 1) / kStreamWaves;
-  if (s > most) s = most;
-  return s < 1 ? 1 : (s > 8 ? 8 : s);
+// 64-wide groups of a split (direct) or of a split's wavefront (stream).
+int part_groups(int T, int N, int K, int splits) {
+  const int over = path_of(T, N, K) == kDirect ? splits : splits * kStreamWaves;
+  return (K / 64 + over - 1) / over;
+}
+// Four 64-wide blocks per wavefront.
+int stream_shrink_splits(int F) {
+  const int s = (F / 64 + 4 * kStreamWaves - 1) / (4 * kStreamWaves);
+  return s > kMaxSplits ? kMaxSplits : s;
 }
 
 struct Carve {
@@ -1064,19 +1504,20 @@ size_t carve(const Layer &L, int matrix, int n, int R, int T, bool backward, voi
   o.Tp = (T + 63) / 64 * 64;
   o.su = shrink_splits(T, (int)K);
   o.sv = shrink_splits(T, (int)N);
-  if (!backward && T <= kStreamRows) {
-    o.sp = stream_splits(T, (int)N, (int)K);
-    o.su = stream_shrink_splits(T, (int)K);
-    o.part = c.take<float>((size_t)o.sp * T * N);
-  } else {
-    o.plane = c.take<uint16_t>(N * K);
-    if (!backward) o.sc = c.take<float>(N * K / 64);
+  const bool stream = (backward ? path_of(T, (int)K, (int)N) : path_of(T, (int)N, (int)K)) != kGemm;
+  if (stream) {  // backward: dx [T][K], contracted over N
+    o.sp = backward ? part_splits(T, (int)K, (int)N) : part_splits(T, (int)N, (int)K);
+    o.su = stream_shrink_splits((int)K);
+    o.sv = stream_shrink_splits((int)N);
+    o.part = c.take<float>((size_t)o.sp * T * (backward ? K : N));
   }
+  if (backward || !stream) o.plane = c.take<uint16_t>(N * K);
+  if (!backward && !stream) o.sc = c.take<float>(N * K / 64);
   if (n) {
     o.part_u = c.take<float>((size_t)o.su * T * o.R32);
     if (backward) {
       o.part_v = c.take<float>((size_t)o.sv * T * o.R32);
-      o.rows = c.take<float>((size_t)T * o.R32);
+      if (!stream) o.rows = c.take<float>((size_t)T * o.R32);
       o.at = c.take<uint16_t>((size_t)n * R * K);
       o.bt = c.take<uint16_t>((size_t)n * R * N);
       o.planes_u = c.take<uint16_t>((size_t)3 * o.R32 * o.Tp);
@@ -1095,24 +1536,42 @@ size_t carve(const Layer &L, int matrix, int n, int R, int T, bool backward, voi
 
 // Workgroups (per tile) that the requests of a tile are spread over.
 int spread(int rows, int n_req) { return n_req < rows ? n_req : rows; }
+// The same for the long requests' 64-row tiles: what a tile holds on average,
+// and one more for tiles that a boundary cuts.
+int spread_long(int T, int n_req) {
+  const int tiles = (T + 63) / 64;
+  return spread(16, n_req < 2 ? n_req : (n_req + tiles - 1) / tiles + 1);
+}
 
 int launch_shrink(const ShrinkArgs &a, const ShrinkArgs &b, hipStream_t s) {
-  const dim3 grid((a.T + 63) / 64, a.nsub, a.splits + b.splits);
-  if (a.R32 <= 32) launch_k(COLI_K_PROJECT_SHRINK, shrink_kernel<2>, grid, dim3(256), 0, s, a, b);
-  else if (a.R32 <= 64) launch_k(COLI_K_PROJECT_SHRINK, shrink_kernel<4>, grid, dim3(256), 0, s, a, b);
-  else launch_k(COLI_K_PROJECT_SHRINK, shrink_kernel<8>, grid, dim3(256), 0, s, a, b);
+  const dim3 grid((a.T + 63) / 64, a.nsub, a.splits + b.splits), block(256);
+  if (a.R32 <= 32) launch_k(COLI_K_PROJECT_SHRINK, shrink_kernel<2>, grid, block, 0, s, a, b);
+  else if (a.R32 <= 64) launch_k(COLI_K_PROJECT_SHRINK, shrink_kernel<4>, grid, block, 0, s, a, b);
+  else launch_k(COLI_K_PROJECT_SHRINK, shrink_kernel<8>, grid, block, 0, s, a, b);
+  return hip_status(hipGetLastError());
+}
+
+template <int BM, int BN, int WM, bool SCALED, bool F32>
+int launch_gemm_cfg(const GemmArgs &g, hipStream_t s) {
+  const unsigned tiles = (unsigned)(((g.N + BN - 1) / BN) * ((g.T + BM - 1) / BM));
+  launch_k(COLI_K_PROJECT_GEMM, gemm_kernel<BM, BN, WM, SCALED, F32>, dim3((tiles + 7) / 8 * 8),
+           dim3(BM / WM * BN), 0, s, g);
   return hip_status(hipGetLastError());
 }
 
 template <bool SCALED, bool F32>
 int launch_gemm(const GemmArgs &g, hipStream_t s) {
-  const dim3 grid((g.N + 127) / 128, (g.T + 127) / 128);
-  launch_k(COLI_K_PROJECT_GEMM, gemm_kernel<128, 128, 64, SCALED, F32>, grid, dim3(256), 0, s, g);
-  return hip_status(hipGetLastError());
+  return launch_gemm_cfg<256, 128, 64, SCALED, F32>(g, s);
 }
 
 template <int F, int RT>
-int launch_stream(const StreamArgs &g, hipStream_t s) {
+int launch_stream(const StreamArgs &g, int N, hipStream_t s) {  // N: the columns the path was chosen for
+  if (path_of(g.T, N, g.m.K) == kDirect) {
+    const int tiles = (g.m.N + kDirectCols - 1) / kDirectCols * ((g.T + kDirectRows - 1) / kDirectRows);
+    launch_k(COLI_K_PROJECT_STREAM, direct_kernel<F, RT>, dim3(g.shrink_blocks + tiles * g.splits),
+             dim3(64 * kDirectWaves), 0, s, g);
+    return hip_status(hipGetLastError());
+  }
   const int mt = stream_mt(g.T);
   const unsigned grid = g.shrink_blocks +
                         g.m.N / (16 * mt) * ((g.T + 16 * mt - 1) / (16 * mt)) * g.splits;
@@ -1123,10 +1582,10 @@ int launch_stream(const StreamArgs &g, hipStream_t s) {
   return hip_status(hipGetLastError());
 }
 template <int F>
-int launch_stream_rank(const StreamArgs &g, int R32, hipStream_t s) {
-  if (R32 <= 32) return launch_stream<F, 2>(g, s);
-  if (R32 <= 64) return launch_stream<F, 4>(g, s);
-  return launch_stream<F, 8>(g, s);
+int launch_stream_rank(const StreamArgs &g, int N, int R32, hipStream_t s) {
+  if (R32 <= 32) return launch_stream<F, 2>(g, N, s);
+  if (R32 <= 64) return launch_stream<F, 4>(g, N, s);
+  return launch_stream<F, 8>(g, N, s);
 }
 
 Requests requests_of(const coli_moe_adapters_t *ad, const coli_moe_requests_t *rq) {
@@ -1164,19 +1623,20 @@ int launch_project(const Layer &L, int expert, int matrix, const coli_moe_adapte
     e.R = ad->max_rank;
     e.R32 = w.R32;
     e.splits = w.su;
-    sh = {x, ad->a, ad->rank, ad->scale, e.q, w.part_u, T, m.K, e.R, e.R32, w.su, 1};
+    sh = {x, ad->a, ad->rank, ad->scale, e.q, w.part_u, T, m.K, e.R, e.R32, w.su,
+          path_of(T, m.N, m.K) == kGemm ? spread_long(T, e.q.n) : spread(16, e.q.n)};
   }
   int rc;
-  if (T <= kStreamRows) {
+  if (path_of(T, m.N, m.K) != kGemm) {
     StreamArgs g = {};
     g.m = m;
     g.x = x;
     g.part = w.part;
     g.T = T;
     g.splits = w.sp;
-    g.per = (m.K / 64 + kStreamWaves * w.sp - 1) / (kStreamWaves * w.sp);
+    g.per = part_groups(T, m.N, m.K, w.sp);
     g.shrink_tiles = (T + 15) / 16;
-    g.s = sh;
+    g.s[0] = sh;
     CombineArgs c = {};
     c.part = w.part;
     c.splits = w.sp;
@@ -1184,12 +1644,12 @@ int launch_project(const Layer &L, int expert, int matrix, const coli_moe_adapte
     c.y = y;
     c.e = e;
     if (ad) {
-      c.nsub = g.s.nsub = spread(16, e.q.n);
-      g.shrink_blocks = g.shrink_tiles * g.s.nsub * w.su;
+      c.nsub = sh.nsub;
+      g.shrink_blocks = g.shrink_tiles * c.nsub * w.su;
     }
-    rc = fmt == kI4 ? launch_stream_rank<kI4>(g, w.R32, s)
-                    : (fmt == kI8 ? launch_stream_rank<kI8>(g, w.R32, s)
-                                  : launch_stream_rank<kF4>(g, w.R32, s));
+    rc = fmt == kI4 ? launch_stream_rank<kI4>(g, m.N, w.R32, s)
+                    : (fmt == kI8 ? launch_stream_rank<kI8>(g, m.N, w.R32, s)
+                                  : launch_stream_rank<kF4>(g, m.N, w.R32, s));
     if (rc) return rc;
     const dim3 grid((m.N + 255) / 256, (T + 15) / 16, c.nsub);
     if (f32) launch_k(COLI_K_PROJECT_COMBINE, combine_parts_kernel<true>, grid, dim3(256), 0, s, c);
@@ -1233,14 +1693,14 @@ int launch_project_backward(const Layer &L, int expert, int matrix, const coli_m
   else if (fmt == kI8) launch_k(COLI_K_PROJECT_PREP, prep_transposed_kernel<kI8>, pg, dim3(256), 0, s, p);
   else launch_k(COLI_K_PROJECT_PREP, prep_transposed_kernel<kF4>, pg, dim3(256), 0, s, p);
   if ((rc = hip_status(hipGetLastError()))) return rc;
+  const bool stream = path_of(T, m.K, m.N) != kGemm;
+  ShrinkArgs u = {}, v = {};
+  FinishArgs f = {};
   if (ad) {
-    const Requests q = p.q;
-    const int nsub = T <= 1024 ? spread(16, q.n) : 1;
-    const ShrinkArgs u = {x, ad->a, ad->rank, ad->scale, q, w.part_u, T, m.K, R, w.R32, w.su, nsub};
-    const ShrinkArgs v = {dy, w.bt, ad->rank, ad->scale, q, w.part_v, T, m.N, R, w.R32, w.sv, nsub};
-    if ((rc = launch_shrink(u, v, s))) return rc;
-    FinishArgs f = {};
-    f.q = q;
+    const int nsub = stream ? spread(16, p.q.n) : spread_long(T, p.q.n);
+    u = {x, ad->a, ad->rank, ad->scale, p.q, w.part_u, T, m.K, R, w.R32, w.su, nsub};
+    v = {dy, w.bt, ad->rank, ad->scale, p.q, w.part_v, T, m.N, R, w.R32, w.sv, nsub};
+    f.q = p.q;
     f.part[0] = w.part_u;
     f.part[1] = w.part_v;
     f.splits[0] = w.su;
@@ -1252,6 +1712,34 @@ int launch_project_backward(const Layer &L, int expert, int matrix, const coli_m
     f.T = T;
     f.Tp = w.Tp;
     f.R32 = w.R32;
+  }
+  if (stream) {
+    StreamArgs g = {};
+    g.m = {reinterpret_cast<const uint8_t *>(w.plane), nullptr, dx ? m.K : 0, m.N};
+    g.x = dy;
+    g.part = w.part;
+    g.T = T;
+    g.splits = w.sp;
+    g.per = part_groups(T, m.K, m.N, w.sp);
+    g.shrink_tiles = (T + 15) / 16;
+    g.s[0] = u;
+    g.s[1] = v;
+    g.shrink_blocks = g.shrink_tiles * u.nsub * (u.splits + v.splits);
+    if ((rc = launch_stream_rank<kBF>(g, m.K, w.R32, s))) return rc;
+    CombineArgs c = {};
+    c.part = w.part;
+    c.splits = w.sp;
+    c.nsub = ad ? u.nsub : 1;
+    c.y = dx;
+    c.e.T = T;
+    c.e.N = m.K;
+    if (ad) c.e = {p.q, w.part_v, w.at, ad->rank, T, m.K, R, w.R32, w.sv};
+    const int cb = dx ? (m.K + 255) / 256 * ((T + 15) / 16) * c.nsub : 0;
+    const int fb = d_a ? w.Tp / 64 * (w.R32 / 32) * 2 : 0;
+    launch_k(COLI_K_PROJECT_COMBINE, combine_finish_kernel, dim3(cb + fb), dim3(256), 0, s, c, f, cb);
+    if ((rc = hip_status(hipGetLastError()))) return rc;
+  } else if (ad) {
+    if ((rc = launch_shrink(u, v, s))) return rc;
     launch_k(COLI_K_PROJECT_FINISH, finish_kernel, dim3(w.Tp / 64, w.R32 / 32, 2), dim3(256), 0, s, f);
     if ((rc = hip_status(hipGetLastError()))) return rc;
   }
@@ -1286,7 +1774,7 @@ int launch_project_backward(const Layer &L, int expert, int matrix, const coli_m
       if ((rc = hip_status(hipGetLastError()))) return rc;
     }
   }
-  if (!dx) return COLI_OK;
+  if (!dx || stream) return COLI_OK;
   ExpandArgs e = {};
   if (ad) e = {p.q, w.rows, w.at, ad->rank, T, m.K, R, w.R32, 1};
   return launch_gemm<false, false>({dy, w.plane, nullptr, T, m.K, m.N, dx, e}, s);
