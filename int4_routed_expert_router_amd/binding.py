@@ -196,14 +196,15 @@ class Route:
         self.c = _RouteC(*[_ptr(getattr(self, n)) for n, _ in _RouteC._fields_])
 
 
-def _need(t, name, dtype, numel, device):
-    """A dense device tensor of this type and at least this many elements, or None."""
-    if t is None:
+def _need(t, name, dtype, numel, dev):
+    """A dense tensor of this type, on GPU `dev` (-1: the CPU), of at least so many elements, or None."""
+    if t is None or (t.dtype is dtype and t.get_device() == dev and t.numel() >= numel
+                     and t.is_contiguous()):
         return
-    if (t.dtype != dtype or t.device != device or t.numel() < numel or not t.is_contiguous()):
-        raise ValueError("%s: expected a contiguous %s tensor of at least %d elements on %s, got "
-                         "%s %s on %s%s" % (name, dtype, numel, device, tuple(t.shape), t.dtype,
-                                            t.device, "" if t.is_contiguous() else " (strided)"))
+    raise ValueError("%s: expected a contiguous %s tensor of at least %d elements on %s, got "
+                     "%s %s on %s%s" % (name, dtype, numel, "cuda:%d" % dev if dev >= 0 else "cpu",
+                                        tuple(t.shape), t.dtype, t.device,
+                                        "" if t.is_contiguous() else " (strided)"))
 
 
 class Adapters:
@@ -216,10 +217,11 @@ class Adapters:
             raise ValueError("adapters: expected a [n, R, K] and b [n, N, R], got %s and %s"
                              % (tuple(a.shape), tuple(b.shape)))
         n, r, k = a.shape
-        _need(a, "a", torch.bfloat16, a.numel(), a.device)
-        _need(b, "b", torch.bfloat16, b.numel(), a.device)
-        _need(rank, "rank", torch.int32, n, a.device)
-        _need(scale, "scale", torch.float32, n, a.device)
+        dev = a.get_device()
+        _need(a, "a", torch.bfloat16, a.numel(), dev)
+        _need(b, "b", torch.bfloat16, b.numel(), dev)
+        _need(rank, "rank", torch.int32, n, dev)
+        _need(scale, "scale", torch.float32, n, dev)
         self.a, self.b, self.rank, self.scale = a, b, rank, scale  # keep the tensors alive
         self.n, self.r, self.k, self.rows = n, r, k, b.shape[1]
         self.c = _AdaptersC(n, r, _ptr(a), _ptr(b), _ptr(rank), _ptr(scale))
@@ -230,8 +232,8 @@ class Requests:
     and adapter [n], int32 on the device (see include/coli_moe.h)."""
 
     def __init__(self, offsets, adapter):
-        _need(adapter, "adapter", torch.int32, 1, adapter.device)
-        _need(offsets, "offsets", torch.int32, adapter.numel() + 1, adapter.device)
+        _need(adapter, "adapter", torch.int32, 1, adapter.get_device())
+        _need(offsets, "offsets", torch.int32, adapter.numel() + 1, adapter.get_device())
         self.offsets, self.adapter = offsets, adapter
         self.c = _RequestsC(adapter.numel(), _ptr(offsets), _ptr(adapter))
 
@@ -250,9 +252,8 @@ class Balance:
         self.tokens = torch.empty(n_seq, dtype=torch.int32, device=device)
         self.totals = torch.empty(2, dtype=torch.int32, device=device)
         self.loss = torch.empty(2, dtype=torch.float32, device=device)
-        device = self.loss.device
-        _need(seq_offsets, "seq_offsets", torch.int32, n_seq + 1, device)
-        _need(valid, "valid", torch.uint8, 1, device)
+        _need(seq_offsets, "seq_offsets", torch.int32, n_seq + 1, self.loss.get_device())
+        _need(valid, "valid", torch.uint8, 1, self.loss.get_device())
         self.c = _BalanceC(n_seq, *[_ptr(getattr(self, n)) for n, _ in _BalanceC._fields_[1:]])
 
 
@@ -380,21 +381,23 @@ def _run(name, on, stream, *args):
     """Calls the library on the device of tensor `on`: by default on that
     device's current stream, which is made current for the call if it is not."""
     fn = getattr(_load(), name)
-    if not on.is_cuda:
+    dev = on.get_device()
+    if dev < 0:
         raise ValueError("%s: tensors have to be on the GPU, got %s" % (name, on.device))
-    s = torch.cuda.current_stream(on.device).cuda_stream if stream is None else _stream(stream)
-    if on.device.index == torch.cuda.current_device():
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    if dev == torch._C._cuda_getDevice():
         rc = fn(*args, s)
     else:
-        with torch.cuda.device(on.device):
+        with torch.cuda.device(dev):
             rc = fn(*args, s)
-    _check(name, rc)
+    if rc != COLI_OK:
+        raise ColiError(name, rc)
 
 
 def _ws(ws, on):
     """Pointer and bytes of a workspace."""
-    _need(ws, "ws", ws.dtype, 0, on.device)
-    return _ptr(ws), ws.numel() * ws.element_size()
+    _need(ws, "ws", ws.dtype, 0, on.get_device())
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def coli_moe_project_workspace_bytes(layer: Layer, matrix: int, adapters, T: int,
@@ -414,37 +417,40 @@ def project_workspace(layer: Layer, matrix: int, adapters, T: int, backward: boo
 
 def _project_args(layer, matrix, adapters, requests, x, T):
     n, k = _shape_nk(layer, matrix)
-    _need(x, "x", torch.bfloat16, T * k, x.device)
-    if adapters is not None and (adapters.k != k or adapters.rows != n):
+    dev = x.get_device()
+    _need(x, "x", torch.bfloat16, T * k, dev)
+    if adapters is None or requests is None:
+        ad = None if adapters is None else ctypes.byref(adapters.c)
+        return n, k, dev, ad, None if requests is None else ctypes.byref(requests.c)
+    if adapters.k != k or adapters.rows != n:
         raise ValueError("adapters of a %d x %d matrix given for a %d x %d one"
                          % (adapters.rows, adapters.k, n, k))
-    for t, name in ((adapters and adapters.a, "adapters"), (requests and requests.adapter, "requests")):
-        if t is not None and t.device != x.device:
-            raise ValueError("%s on %s, x on %s" % (name, t.device, x.device))
-    return n, k, (None if adapters is None else ctypes.byref(adapters.c),
-                  None if requests is None else ctypes.byref(requests.c))
+    if adapters.a.get_device() != dev or requests.adapter.get_device() != dev:
+        raise ValueError("adapters on %s, requests on %s, x on %s"
+                         % (adapters.a.device, requests.adapter.device, x.device))
+    return n, k, dev, ctypes.byref(adapters.c), ctypes.byref(requests.c)
 
 
 def coli_moe_project(layer: Layer, expert: int, matrix: int, adapters, requests, x, T: int, y,
                      y_dtype: int, ws, stream=None):
     """y = x W^T + the requests' adapters (adapters and requests may both be None)."""
-    n, _, (ad, rq) = _project_args(layer, matrix, adapters, requests, x, T)
-    _need(y, "y", torch.float32 if y_dtype == COLI_OUT_F32 else torch.bfloat16, T * n, x.device)
-    _run("coli_moe_project", x, stream, ctypes.byref(layer.c), expert, matrix, ad, rq, _ptr(x), T,
-         _ptr(y), y_dtype, *_ws(ws, x))
+    n, _, dev, ad, rq = _project_args(layer, matrix, adapters, requests, x, T)
+    _need(y, "y", torch.float32 if y_dtype == COLI_OUT_F32 else torch.bfloat16, T * n, dev)
+    _run("coli_moe_project", x, stream, ctypes.byref(layer.c), expert, matrix, ad, rq,
+         x.data_ptr(), T, y.data_ptr(), y_dtype, *_ws(ws, x))
 
 
 def coli_moe_project_backward(layer: Layer, expert: int, matrix: int, adapters, requests, x, dy,
                               T: int, dx, d_a, d_b, ws, stream=None):
     """dx (bf16), d_a and d_b (fp32) of coli_moe_project; dx, or d_a and d_b, may be None."""
-    n, k, (ad, rq) = _project_args(layer, matrix, adapters, requests, x, T)
-    _need(dy, "dy", torch.bfloat16, T * n, x.device)
-    _need(dx, "dx", torch.bfloat16, T * k, x.device)
+    n, k, dev, ad, rq = _project_args(layer, matrix, adapters, requests, x, T)
+    _need(dy, "dy", torch.bfloat16, T * n, dev)
+    _need(dx, "dx", torch.bfloat16, T * k, dev)
     if adapters is not None:
-        _need(d_a, "d_a", torch.float32, adapters.a.numel(), x.device)
-        _need(d_b, "d_b", torch.float32, adapters.b.numel(), x.device)
+        _need(d_a, "d_a", torch.float32, adapters.a.numel(), dev)
+        _need(d_b, "d_b", torch.float32, adapters.b.numel(), dev)
     _run("coli_moe_project_backward", x, stream, ctypes.byref(layer.c), expert, matrix, ad, rq,
-         _ptr(x), _ptr(dy), T, _ptr(dx), _ptr(d_a), _ptr(d_b), *_ws(ws, x))
+         x.data_ptr(), dy.data_ptr(), T, _ptr(dx), _ptr(d_a), _ptr(d_b), *_ws(ws, x))
 
 
 def coli_moe_balance_workspace_bytes(layer: Layer, T: int, n_seq: int = 1) -> int:
@@ -458,32 +464,33 @@ def balance_workspace(layer: Layer, T: int, n_seq: int = 1, device="cuda") -> to
 
 
 def _balance_args(layer, logits, topk_idx, T, balance):
-    _need(logits, "logits", torch.float32, T * layer.n_experts, logits.device)
-    _need(topk_idx, "topk_idx", torch.int32, T * layer.top_k, logits.device)
+    dev, E = logits.get_device(), layer.n_experts
+    _need(logits, "logits", torch.float32, T * E, dev)
+    _need(topk_idx, "topk_idx", torch.int32, T * layer.top_k, dev)
     if balance is not None:
-        _need(balance.valid, "valid", torch.uint8, T, logits.device)
-        _need(balance.counts, "balance", torch.int32, balance.c.n_seq * layer.n_experts,
-              logits.device)
+        _need(balance.valid, "valid", torch.uint8, T, dev)
+        _need(balance.counts, "balance", torch.int32, balance.c.n_seq * E, dev)
+    return dev
 
 
 def coli_moe_balance_loss(layer: Layer, logits, topk_idx, T: int, balance: Balance, ws,
                           stream=None):
     _balance_args(layer, logits, topk_idx, T, balance)
-    _run("coli_moe_balance_loss", logits, stream, ctypes.byref(layer.c), _ptr(logits),
-         _ptr(topk_idx), T, ctypes.byref(balance.c), *_ws(ws, logits))
+    _run("coli_moe_balance_loss", logits, stream, ctypes.byref(layer.c), logits.data_ptr(),
+         topk_idx.data_ptr(), T, ctypes.byref(balance.c), *_ws(ws, logits))
 
 
 def coli_moe_route_backward(layer: Layer, logits, topk_idx, T: int, d_topk_w, balance, d_loss,
                             d_logits, stream=None):
     """d_logits of the routing weights (d_topk_w) and of the balance and z-losses
     (balance, d_loss); either part may be None."""
-    _balance_args(layer, logits, topk_idx, T, balance)
-    _need(d_topk_w, "d_topk_w", torch.float32, T * layer.top_k, logits.device)
-    _need(d_loss, "d_loss", torch.float32, 2, logits.device)
-    _need(d_logits, "d_logits", torch.float32, T * layer.n_experts, logits.device)
-    _run("coli_moe_route_backward", logits, stream, ctypes.byref(layer.c), _ptr(logits),
-         _ptr(topk_idx), T, _ptr(d_topk_w), None if balance is None else ctypes.byref(balance.c),
-         _ptr(d_loss), _ptr(d_logits))
+    dev = _balance_args(layer, logits, topk_idx, T, balance)
+    _need(d_topk_w, "d_topk_w", torch.float32, T * layer.top_k, dev)
+    _need(d_loss, "d_loss", torch.float32, 2, dev)
+    _need(d_logits, "d_logits", torch.float32, T * layer.n_experts, dev)
+    _run("coli_moe_route_backward", logits, stream, ctypes.byref(layer.c), logits.data_ptr(),
+         topk_idx.data_ptr(), T, _ptr(d_topk_w),
+         None if balance is None else ctypes.byref(balance.c), _ptr(d_loss), d_logits.data_ptr())
 
 
 def _hip_runtime():

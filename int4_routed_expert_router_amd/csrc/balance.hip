@@ -155,6 +155,9 @@ COLI_DEV void row_probs(const float (&l)[N], Row<N> &o) {
   for (int i = 0; i < N; ++i) o.p[i] *= inv;
 }
 
+// Choices of a row that a lane holds: k <= min(E, 32).
+constexpr int lane_choices(int W) { return W >= 32 ? 1 : (W == 16 ? 2 : 4); }
+
 // ---------------------------------------------------------------- forward
 
 struct FwdArgs {
@@ -280,17 +283,19 @@ __device__ void finish_sequences(const FwdArgs &g, FinShared &sh, int block, int
   }
   block_sums(term, live, sh);
   if (!solo) {
-    // the partial sums pass between workgroups of different L2s: device
-    // scope on both sides of the ticket
+    // The partial sums pass between workgroups of different L2s: device-scope
+    // stores and loads, which go past the L2s, and between store and ticket a
+    // wait until the stores are done.  (A fence would also write back what
+    // else is in the L2s, which nobody here reads.)
     if (tid == 0) {
       __hip_atomic_store(&g.fin_term[block], term, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       __hip_atomic_store(&g.fin_live[block], live, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      __threadfence();
-      sh.last = atomicAdd(g.ticket, 1u) == (uint32_t)n_blocks - 1u;
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      sh.last = __hip_atomic_fetch_add(g.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                (uint32_t)n_blocks - 1u;
     }
     __syncthreads();
     if (!sh.last) return;
-    __threadfence();
     term = 0.0;
     live = 0;
     for (int i = tid; i < n_blocks; i += kFwdThreads) {
@@ -347,20 +352,31 @@ __global__ void __launch_bounds__(kFwdThreads) balance_kernel(FwdArgs g) {
       if (tid == 0) counted = 0;
       __syncthreads();
       int mine = 0;
-      float l[C * V];
-      int t = pos + grp;
-      if (t < end) load_row<W, C, V>(g.logits + (int64_t)t * E, E, gl, l);
-      for (; t < end; t += G) {
-        float next[C * V];  // the next row, on its way while this one is summed
-        const int tn = min(t + G, end - 1);
-        load_row<W, C, V>(g.logits + (int64_t)tn * E, E, gl, next);
-        if (!g.valid || g.valid[t]) {
-          for (int j = gl; j < g.k; j += W) {
-            const int e = g.idx[(int64_t)t * g.k + j];
-            if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
-          }
+      // the next row's inputs are on their way while this one is summed
+      constexpr int KL = lane_choices(W);
+      struct In {
+        float l[C * V];
+        int e[KL];
+        int valid;
+      };
+      auto fetch = [&](int t, In &o) {
+        t = min(t, end - 1);
+        load_row<W, C, V>(g.logits + (int64_t)t * E, E, gl, o.l);
+#pragma unroll
+        for (int i = 0; i < KL; ++i)
+          o.e[i] = gl + W * i < g.k ? g.idx[(int64_t)t * g.k + gl + W * i] : -1;
+        o.valid = g.valid ? g.valid[t] : 1;
+      };
+      In cur, next;
+      fetch(pos + grp, cur);
+      for (int t = pos + grp; t < end; t += G) {
+        fetch(t + G, next);
+        if (cur.valid) {
+#pragma unroll
+          for (int i = 0; i < KL; ++i)
+            if (cur.e[i] >= 0 && cur.e[i] < E) atomicAdd(&hist[cur.e[i]], 1);
           Row<C * V> r;
-          row_probs<W, C * V, SIGMOID>(l, r);
+          row_probs<W, C * V, SIGMOID>(cur.l, r);
 #pragma unroll
           for (int i = 0; i < C * V; ++i) acc[i] += r.p[i];
           if (gl == 0) {
@@ -368,8 +384,7 @@ __global__ void __launch_bounds__(kFwdThreads) balance_kernel(FwdArgs g) {
             ++mine;
           }
         }
-#pragma unroll
-        for (int i = 0; i < C * V; ++i) l[i] = next[i];
+        cur = next;
       }
       if (gl == 0 && mine) atomicAdd(&counted, mine);
 #pragma unroll
@@ -516,7 +531,7 @@ template <int W, int C, int V, bool SIGMOID, bool RENORM>
 __global__ void __launch_bounds__(kBwdThreads) route_backward_kernel(BwdArgs g) {
   constexpr int G = 64 / W;  // rows of a wavefront in flight
   constexpr int S = W * C * V;
-  constexpr int KL = W >= 32 ? 1 : (W == 16 ? 2 : 4);  // choices per lane: k <= min(E, 32)
+  constexpr int KL = lane_choices(W);
   __shared__ __align__(16) float grads[kBwdThreads / W][S];
   __shared__ __align__(16) float logit[kBwdThreads / W][S];
   const int lane = threadIdx.x & 63, gl = lane % W, grp = lane / W;

@@ -1180,9 +1180,16 @@ __global__ void __launch_bounds__(256) combine_parts_kernel(CombineArgs g) {
 
 // ----------------------------------------------------------------- finish
 
+// Index of a lane's eight values of part p in the planes of u and v.
+COLI_DEV int64_t plane_at(int window, int p, int rank_tile, int R32, int lane) {
+  return (((int64_t)window * 3 + p) * (R32 / 16) + rank_tile) * 64 + lane;
+}
+
 // Sums shrink's parts of u and v.  Writes v as rows (fp32 [T][R32]), both
-// transposed as three bf16 parts [3][R32][Tp], and every row's adapter;
-// zeros for rows without one.
+// as three bf16 parts in the order of the matrix-core operands that grads
+// loads -- [Tp/32][3][R32/16][lane][8 rows], lane (c, g) holding rows 8g .. 8g
+// + 7 of a window of 32 at rank c: whole KiBs instead of 16-byte pieces of 16
+// lines -- and every row's adapter; zeros for rows without one.
 struct FinishArgs {
   Requests q;
   const float *part[2];  // u, v
@@ -1235,7 +1242,8 @@ COLI_DEV void finish_tile(const FinishArgs &g, int tile, int rank_block, int w) 
   split8<3>(v, parts);
 #pragma unroll
   for (int p = 0; p < 3; ++p)
-    *reinterpret_cast<uint4 *>(g.planes[w] + ((int64_t)p * g.R32 + r0 + r) * g.Tp + t0 + tt) = parts[p];
+    reinterpret_cast<uint4 *>(g.planes[w])[plane_at((t0 + tt) / 32, p, (r0 + r) / 16, g.R32,
+                                                    (tt % 32) / 8 * 16 + r % 16)] = parts[p];
 }
 
 __global__ void __launch_bounds__(256) finish_kernel(FinishArgs g) {
@@ -1261,7 +1269,7 @@ __global__ void __launch_bounds__(256) combine_finish_kernel(CombineArgs c, Fini
 // G_a[f][r] = sum over a's rows t of z[t][f] p[t][r].
 struct GradArgs {
   const uint16_t *z;       // [T][F]
-  const uint16_t *planes;  // [3][R32][Tp]
+  const uint16_t *planes;  // see finish_tile
   float *out;              // [splits][n][R][F] (dA) or [splits][n][F][R] (dB)
   int F;
   int transposed;          // dB's layout
@@ -1323,8 +1331,8 @@ __global__ void __launch_bounds__(256) grads_kernel(GradsArgs a) {
       for (int p = 0; p < 3; ++p)
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-          const int rr = r0 + 16 * r + c;
-          uint4 v = rr < a.R32 ? ld16(g.planes + ((int64_t)p * a.R32 + rr) * a.Tp + t) : zero4();
+          const int rt = min(r0 / 16 + r, a.R32 / 16 - 1);  // ranks past R32 are not stored
+          uint4 v = reinterpret_cast<const uint4 *>(g.planes)[plane_at(w0 / 32 + h, p, rt, a.R32, lane)];
           // other adapters' rows may hold anything
           if (m32 != 0xffffffffu) {
             uint32_t d[4] = {v.x, v.y, v.z, v.w};
@@ -1422,11 +1430,13 @@ int shrink_splits(int T, int F) {
   if (s > F / 256) s = F / 256;
   return s < 1 ? 1 : (s > kMaxSplits ? kMaxSplits : s);
 }
-// Row ranges of the gradients: about 1,024 workgroups.
+// Row ranges of the gradients: about 512 workgroups, two to a CU (8192 rows,
+// two adapters of rank 64, 6144 and 2048 columns: 26.8 us, against 37.8 us with
+// 1,024 and 32.8 us with 256).
 int grad_splits(int T, int N, int K, int n) {
   const int64_t blocks = (int64_t)((N + 127) / 128 + (K + 127) / 128) * n;
   const int windows = (T + 255) / 256;  // a window per wavefront
-  int64_t s = (1024 + blocks - 1) / blocks;
+  int64_t s = (512 + blocks - 1) / blocks;
   if (s > windows) s = windows;
   return (int)(s > 16 ? 16 : s);
 }
@@ -1467,10 +1477,10 @@ int part_groups(int T, int N, int K, int splits) {
   const int over = path_of(T, N, K) == kDirect ? splits : splits * kStreamWaves;
   return (K / 64 + over - 1) / over;
 }
-// Four 64-wide blocks per wavefront.
-int stream_shrink_splits(int F) {
-  const int s = (F / 64 + 4 * kStreamWaves - 1) / (4 * kStreamWaves);
-  return s > kMaxSplits ? kMaxSplits : s;
+// Four 64-wide blocks per wavefront of u's and v's workgroups beside the parts.
+int part_shrink_splits(int T, int N, int K, int F) {
+  const int waves = path_of(T, N, K) == kDirect ? kDirectWaves : kStreamWaves;
+  return clamp_splits((F / 64 + 4 * waves - 1) / (4 * waves), kMaxSplits);
 }
 
 struct Carve {
@@ -1507,8 +1517,9 @@ size_t carve(const Layer &L, int matrix, int n, int R, int T, bool backward, voi
   const bool stream = (backward ? path_of(T, (int)K, (int)N) : path_of(T, (int)N, (int)K)) != kGemm;
   if (stream) {  // backward: dx [T][K], contracted over N
     o.sp = backward ? part_splits(T, (int)K, (int)N) : part_splits(T, (int)N, (int)K);
-    o.su = stream_shrink_splits((int)K);
-    o.sv = stream_shrink_splits((int)N);
+    const int n_out = (int)(backward ? K : N), n_in = (int)(backward ? N : K);
+    o.su = part_shrink_splits(T, n_out, n_in, (int)K);
+    o.sv = part_shrink_splits(T, n_out, n_in, (int)N);
     o.part = c.take<float>((size_t)o.sp * T * (backward ? K : N));
   }
   if (backward || !stream) o.plane = c.take<uint16_t>(N * K);
