@@ -436,8 +436,9 @@ typedef struct coli_moe_adapters {
 } coli_moe_adapters_t;
 
 /* Bytes of workspace of coli_moe_project (backward = 0) or
- * coli_moe_project_backward (backward != 0); adapters may be NULL, and only
- * its n_adapters and max_rank are read.  0 for invalid arguments.  Host-only. */
+ * coli_moe_project_backward (backward != 0) for T rows; it also does for fewer
+ * rows.  adapters may be NULL, and only its n_adapters and max_rank are read.
+ * 0 for invalid arguments.  Host-only. */
 size_t coli_moe_project_workspace_bytes(const coli_moe_layer_t *layer, int32_t matrix,
                                         const coli_moe_adapters_t *adapters, int32_t T,
                                         int32_t backward);
@@ -504,7 +505,8 @@ typedef struct coli_moe_balance {
   float *loss;
 } coli_moe_balance_t;
 
-/* Bytes of workspace of coli_moe_balance_loss; 0 for invalid arguments. */
+/* Bytes of workspace of coli_moe_balance_loss (the same for every T and
+ * n_seq of a layer); 0 for invalid arguments.  Host-only. */
 size_t coli_moe_balance_workspace_bytes(const coli_moe_layer_t *layer, int32_t T, int32_t n_seq);
 
 /* Balance loss, z-loss and per-expert counts of a routed batch.  Reads E, k

@@ -374,8 +374,8 @@ size_t coli_moe_project_workspace_bytes(const coli_moe_layer_t *layer, int32_t m
   Layer L;
   if (check_layer(layer, &L) || matrix < 0 || matrix > 2 || T < 1 || T > kMaxT) return 0;
   if (adapters && check_adapter_sizes(adapters)) return 0;
-  return project_workspace(L, matrix, adapters ? adapters->n_adapters : 0,
-                           adapters ? adapters->max_rank : 0, T, backward);
+  return project_workspace_upto(L, matrix, adapters ? adapters->n_adapters : 0,
+                                adapters ? adapters->max_rank : 0, T, backward);
 }
 
 int coli_moe_project(const coli_moe_layer_t *layer, int32_t expert, int32_t matrix,

@@ -75,6 +75,8 @@ int launch_mx_dots(const Layer &L, int expert, int matrix, const uint8_t *qa, co
 // both given or both NULL.
 size_t project_workspace(const Layer &L, int matrix, int n_adapters, int max_rank, int T,
                          int backward);
+size_t project_workspace_upto(const Layer &L, int matrix, int n_adapters, int max_rank, int T,
+                              int backward);
 int launch_project(const Layer &L, int expert, int matrix, const coli_moe_adapters_t *ad,
                    const coli_moe_requests_t *rq, const uint16_t *x, int T, void *y, int y_dtype,
                    void *ws, hipStream_t s);

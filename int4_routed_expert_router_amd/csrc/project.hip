@@ -191,6 +191,7 @@ struct PrepT {
   uint16_t *at, *bt;  // [n][K][R], [n][R][N]
   int w_tiles, a_tiles, b_tiles;  // workgroups of each kind (a, b per adapter)
 };
+constexpr int kMaxLook = 1024;  // requests that each workgroup looks through
 template <int F>
 __global__ void __launch_bounds__(256) prep_transposed_kernel(PrepT g) {
   __shared__ uint16_t t[64][66];
@@ -221,12 +222,15 @@ __global__ void __launch_bounds__(256) prep_transposed_kernel(PrepT g) {
     b -= g.w_tiles;
     const int per = g.a_tiles + g.b_tiles, a = b / per;
     b %= per;
-    if (tid == 0) used = 0;
-    __syncthreads();
-    for (int i = tid; i < g.q.n; i += 256)
-      if (g.q.adapter[i] == a && g.q.off[i + 1] > g.q.off[i]) used = 1;
-    __syncthreads();
-    if (!used) return;
+    // adapters that no request names are left out where looking is cheap
+    if (g.q.n <= kMaxLook) {
+      if (tid == 0) used = 0;
+      __syncthreads();
+      for (int i = tid; i < g.q.n; i += 256)
+        if (g.q.adapter[i] == a && g.q.off[i + 1] > g.q.off[i]) used = 1;
+      __syncthreads();
+      if (!used) return;
+    }
     const int R = g.ad.R;
     if (b < g.a_tiles) {
       const int ct = g.m.K / 64;
@@ -1456,6 +1460,7 @@ Path path_of(int T, int N, int K) {
   const int tiles = (T + 255) / 256 * ((N + 127) / 128);
   return T > 512 && tiles >= 96 ? kGemm : kDirect;
 }
+constexpr int kLastPartRows = 96 * 256;  // from here on one column of tiles is enough
 // The streaming path's tiles: columns per workgroup grow with the rows, so
 // that x is not read once per 16 columns.
 int stream_mt(int T) { return T <= 16 ? 1 : (T <= 32 ? 2 : 4); }
@@ -1612,6 +1617,18 @@ Requests requests_of(const coli_moe_adapters_t *ad, const coli_moe_requests_t *r
 
 size_t project_workspace(const Layer &L, int matrix, int n, int R, int T, int backward) {
   return carve(L, matrix, n, R, T, backward != 0, nullptr, nullptr);
+}
+
+// The most that any batch of up to T rows needs: the parts of a batch in
+// between can take more than a long batch's unpacked weights.  Sizes grow
+// with T between multiples of 16 (every tile's and path's bound is one).
+size_t project_workspace_upto(const Layer &L, int matrix, int n, int R, int T, int backward) {
+  size_t most = project_workspace(L, matrix, n, R, T, backward);
+  for (int t = 16; t < T && t <= kLastPartRows; t += 16) {
+    const size_t need = project_workspace(L, matrix, n, R, t, backward);
+    if (need > most) most = need;
+  }
+  return most;
 }
 
 int launch_project(const Layer &L, int expert, int matrix, const coli_moe_adapters_t *ad,

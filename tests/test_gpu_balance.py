@@ -272,3 +272,59 @@ def test_same_bits_twice_and_misaligned_rows():
     c = _run(L, odd, idx, T)
     assert torch.equal(c.counts, a.counts)
     assert torch.allclose(c.mean_prob, a.mean_prob, rtol=(2 * 20 + E + T + 32) * E24, atol=0)
+
+
+def test_captured_calls_replay():
+    """Loss and gradient captured together and replayed with new logits."""
+    T, E, k = 777, 64, 4
+    L = _layer(E, k, True, True)
+    off = torch.tensor([0, 100, 777], dtype=torch.int32).cuda()
+    l, idx = _inputs(T, E, k)
+    l, idx = l.cuda(), idx.cuda()
+    b = coli.Balance(L, 2, off)
+    ws = coli.balance_workspace(L, T, 2)
+    dw, d_loss = torch.randn(T, k, device="cuda"), torch.rand(2, device="cuda")
+    dl = torch.empty(T, E, device="cuda")
+
+    def step():
+        coli.coli_moe_balance_loss(L, l, idx, T, b, ws)
+        coli.coli_moe_route_backward(L, l, idx, T, dw, b, d_loss, dl)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for i in range(5):
+        l.copy_(_inputs(T, E, k, seed=50 + i)[0])
+        idx.copy_(l.topk(k, dim=1).indices)
+        step()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (b.loss, b.counts, b.mean_prob, b.tokens, dl)]
+        for t in (b.loss, b.counts, b.mean_prob, b.tokens, dl):
+            t.fill_(-1)
+        ws.fill_(0xff)
+        g.replay()
+        torch.cuda.synchronize()
+        for a, w in zip((b.loss, b.counts, b.mean_prob, b.tokens, dl), want):
+            assert torch.equal(a, w), i
+
+
+def test_an_expert_named_twice_counts_twice():
+    T, E, k = 70, 16, 3
+    L = _layer(E, k, False)
+    l, idx = _inputs(T, E, k)
+    idx[:, 2] = idx[:, 0]
+    b = _run(L, l, idx, T)
+    ih = idx.numpy().astype(np.int64)
+    assert np.array_equal(b.counts.cpu().numpy()[0], np.bincount(ih.reshape(-1), minlength=E))
+    dw = torch.randn(T, k)
+    dl = torch.empty(T, E, device="cuda")
+    coli.coli_moe_route_backward(L, l.cuda(), idx.cuda(), T, dw.cuda(), None, None, dl)
+    ref = tu.route_backward(tu.host(l), ih, False, False, 1.0, tu.host(dw))
+    S = _grad_scale(tu.host(l), ih, False, False, 1.0, tu.host(dw), None, None)
+    assert (np.abs(tu.host(dl) - ref) <= (4 * 20 + 2 * E + 64) * E24 * S + 1e-35).all()

@@ -269,3 +269,139 @@ def test_gradients_match_differences():
             kw = "a" if M is A else "b"
             d = (loss(x, i, **{kw: p}) - loss(x, i, **{kw: m})) / (2 * h)
             assert abs(d - G[at]) < 1e-6 * (1 + abs(G[at]))
+
+
+@pytest.mark.parametrize("T", [7, 70, 1300])
+def test_extreme_weight_scales(T):
+    """fp16 scales down to the smallest subnormal, E8M0 scales near both ends."""
+    print("extreme scales", T, flush=True)
+    for fmt, lo, hi, shift in (("int4", 0, 0, 0), ("int8", 0, 0, 0), ("mxfp4", 1, 12, 90),
+                               ("mxfp4", 240, 251, -100)):
+        spec = _spec(fmt, 2048, 512)
+        c = Case(spec, 2, T, [0, T], [0], tu.Low(1, 8, 2048, 512), seed=3)
+        g = torch.Generator().manual_seed(T)
+        if fmt == "mxfp4":
+            sc = torch.randint(lo, hi, c.sc.shape, generator=g, dtype=torch.uint8)
+        else:
+            bits = torch.randint(1, 0x0420, c.sc.shape, generator=g, dtype=torch.int32)
+            sc = bits.to(torch.int16).view(torch.float16)  # subnormals and the first normals
+        c.sc.copy_(sc)
+        c.w = tu.dense(spec, c.q4.cpu(), sc, c.expert, 2)
+        c.x = (c.x.double() * 2.0 ** shift).to(torch.bfloat16)
+        c.low.a = (c.low.a.double() * 2.0 ** -shift).to(torch.bfloat16)
+        c.ad = c.low.device()
+        c.check_forward()
+
+
+def _captured(fn):
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        fn()  # the first launches outside the capture
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fn()
+    torch.cuda.synchronize()
+    return g
+
+
+@pytest.mark.parametrize("T", [5, 90, 1500])
+def test_captured_calls_replay(T):
+    """Forward and backward captured into two graphs that share a workspace,
+    replayed in turn with new inputs and eager calls in between."""
+    print("graphs", T, flush=True)
+    N = 2048 if T > 1000 else 128
+    spec = _spec("int4", 256, N)
+    low = tu.Low(2, 16, N, 256, ranks=(16, 7))
+    c = Case(spec, 0, T, [0, T // 2, T], [1, 0], low)
+    x, dy = c.x.cuda(), c.dy.cuda()
+    y = torch.empty(T, N, device="cuda")
+    dx = torch.empty(T, 256, dtype=torch.bfloat16, device="cuda")
+    da, db = torch.empty(low.a.shape, device="cuda"), torch.empty(low.b.shape, device="cuda")
+    ws = coli.project_workspace(c.L, 0, c.ad, T, True)
+    wf = coli.project_workspace(c.L, 0, c.ad, T)
+    ws = ws if ws.numel() > wf.numel() else wf
+
+    def forward():
+        coli.coli_moe_project(c.L, c.expert, 0, c.ad, c.rq, x, T, y, coli.COLI_OUT_F32, ws)
+
+    def backward():
+        coli.coli_moe_project_backward(c.L, c.expert, 0, c.ad, c.rq, x, dy, T, dx, da, db, ws)
+
+    gf, gb = _captured(forward), _captured(backward)
+    for i in range(4):
+        g = torch.Generator().manual_seed(100 + i)
+        x.copy_(torch.randn(T, 256, generator=g))
+        dy.copy_(torch.randn(T, N, generator=g))
+        forward()
+        backward()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (y, dx, da, db)]
+        for t in (y, dx, da, db):
+            t.fill_(-1.0)
+        if i % 2:
+            ws.fill_(0xff)
+        gb.replay()
+        gf.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((y, dx, da, db), want):
+            assert torch.equal(a, b), i
+
+
+def test_two_streams_at_once():
+    """Calls on two streams with a workspace each do not disturb each other."""
+    cases = [Case(_spec(f), 0, 300, [0, 100, 300], [0, 1], tu.Low(2, 16, 128, 256, seed=i), seed=i)
+             for i, f in enumerate(("int4", "mxfp4"))]
+    ref = [c.forward() for c in cases]
+    st = [torch.cuda.Stream() for _ in cases]
+    xs = [c.x.cuda() for c in cases]
+    ys = [torch.empty_like(r) for r in ref]
+    ws = [coli.project_workspace(c.L, 0, c.ad, 300) for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, c in enumerate(cases):
+            coli.coli_moe_project(c.L, c.expert, 0, c.ad, c.rq, xs[i], 300, ys[i],
+                                  coli.COLI_OUT_F32, ws[i], stream=st[i])
+    torch.cuda.synchronize()
+    for y, r in zip(ys, ref):
+        assert torch.equal(y, r)
+
+
+@pytest.mark.parametrize("T", [1, 33, 129, 600])
+def test_workspace_for_more_rows_serves_fewer(T):
+    low = tu.Low(2, 16, 128, 256)
+    c = Case(_spec("int4"), 0, T, [0, T], [1], low)
+    ws = coli.project_workspace(c.L, 0, c.ad, 5000)
+    assert torch.equal(c.forward(ws=ws), c.forward())
+
+
+@pytest.mark.parametrize("fmt", ["int4", "int8", "mxfp4"])
+def test_long_batches_match_reference(fmt):
+    """Batches that take the tiled product: whole and cut tiles, an odd number
+    of 64-wide stages, many short requests between long ones."""
+    print("long", fmt, flush=True)
+    for (H, I), T in (((320, 4096), 700), ((192, 2112), 1555)):
+        spec = _spec(fmt, H, I)
+        off = [0, 3, 300] + list(range(301, 340)) + [600, T - 7]
+        who = [(5 * i) % 4 - 1 for i in range(len(off) - 1)]
+        low = tu.Low(3, 24, I, H, ranks=(24, 9, 17))
+        c = Case(spec, 0, T, off, who, low, seed=T)
+        c.check_forward()
+        c.check_backward()
+        low = tu.Low(3, 24, H, I, ranks=(24, 9, 17))
+        c = Case(spec, 2, T, off, who, low, seed=T)
+        c.check_forward()
+        c.check_backward()  # dx [T, I] of the wide side
+
+
+def test_thousands_of_requests():
+    """More requests than the backward pass looks through per adapter."""
+    T = 2000
+    off = list(range(0, T + 1))
+    who = [(7 * i) % 9 - 1 for i in range(T)]
+    low = tu.Low(8, 8, 128, 256)
+    c = Case(_spec("int4"), 0, T, off, who, low)
+    c.check_forward()
+    c.check_backward()

@@ -188,3 +188,19 @@ def test_binding_refuses_tensors_that_do_not_fit():
         coli.coli_moe_balance_loss(L, lg, idx.long(), 8, coli.Balance(L, device="cpu"), ws)
     with pytest.raises(ValueError):
         coli.coli_moe_route_backward(L, lg, idx, 8, torch.zeros(8, 1), None, None, lg)
+
+
+def test_workspace_of_a_batch_does_for_smaller_ones():
+    """The paths of short, middle and long batches need different buffers."""
+    lib = binding.raw_library()
+    ws = lib.coli_moe_project_workspace_bytes
+    for hidden, inter in ((6144, 2048), (256, 128), (64, 16384)):
+        L, a = layer(hidden=hidden, inter=inter), adapters()
+        for matrix in (0, 2):
+            for back in (0, 1):
+                last = 0
+                for T in (1, 16, 17, 32, 33, 100, 128, 129, 512, 513, 1000, 1536, 4000, 24576, 24577,
+                          65536):
+                    n = ws(ctypes.byref(L.c), matrix, ctypes.byref(a), T, back)
+                    assert n >= last > -1, (hidden, matrix, back, T)
+                    last = n
