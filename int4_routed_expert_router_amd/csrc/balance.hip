@@ -127,23 +127,47 @@ struct Row {
   float p[N], e1[N], c[N];
   float m, inv, lse;  // inv: 1 / sum of e1
 };
+// `f` given: also *dot = sum_e f_e p_e.
 template <int W, int N, bool SIGMOID>
-COLI_DEV void row_probs(const float (&l)[N], Row<N> &o) {
+COLI_DEV void row_probs(const float (&l)[N], Row<N> &o, const float *f = nullptr,
+                        float *dot = nullptr) {
   float m = l[0];
 #pragma unroll
   for (int i = 1; i < N; ++i) m = fmaxf(m, l[i]);
   m = max_w<W>(m);
   const bool any = m > -INFINITY;
   float s = 0.0f, z = 0.0f;
+  if (SIGMOID && fabsf(m) <= 80.0f) {
+    // one exponential for both: e^l stays in range (the largest is e^80, and
+    // what underflows below is nothing beside the row's largest), and 1 /
+    // (1 + e^l) and e^l / (1 + e^l) are exact to a few steps
+    const float em = __expf(-m);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    o.e1[i] = any ? __expf(l[i] - m) : 0.0f;
-    s += o.e1[i];
-    Sig g = {};
-    if (SIGMOID) g = sigmoid(l[i]);
-    o.c[i] = g.c;
-    o.p[i] = any ? score<SIGMOID>(g, m, o.e1[i]) : 0.0f;
-    if (SIGMOID) z += o.p[i];
+    for (int i = 0; i < N; ++i) {
+      const float t = __expf(l[i]);
+      o.c[i] = rcp(1.0f + t);
+      o.p[i] = t * o.c[i];
+      o.e1[i] = t * em;
+      s += o.e1[i];
+      z += o.p[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      o.e1[i] = any ? __expf(l[i] - m) : 0.0f;
+      s += o.e1[i];
+      Sig g = {};
+      if (SIGMOID) g = sigmoid(l[i]);
+      o.c[i] = g.c;
+      o.p[i] = any ? score<SIGMOID>(g, m, o.e1[i]) : 0.0f;
+      if (SIGMOID) z += o.p[i];
+    }
+  }
+  float fp = 0.0f;
+  if (f) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) fp += f[i] * o.p[i];
+    fp = sum_w<W>(fp);
   }
   s = sum_w<W>(s);
   z = SIGMOID ? sum_w<W>(z) : s;
@@ -153,6 +177,7 @@ COLI_DEV void row_probs(const float (&l)[N], Row<N> &o) {
   const float inv = any ? rcp(z) : 0.0f;
 #pragma unroll
   for (int i = 0; i < N; ++i) o.p[i] *= inv;
+  if (f) *dot = fp * inv;
 }
 
 // Choices of a row that a lane holds: k <= min(E, 32).
@@ -598,12 +623,9 @@ __global__ void __launch_bounds__(kBwdThreads) route_backward_kernel(BwdArgs g) 
         Row<C * V> r;
         r.m = r.inv = 0.0f;
         if (full) {
-          row_probs<W, C * V, SIGMOID>(l, r);
+          float dot;
+          row_probs<W, C * V, SIGMOID>(l, r, f, &dot);
           if (balance) {
-            float dot = 0.0f;
-#pragma unroll
-            for (int i = 0; i < C * V; ++i) dot += f[i] * r.p[i];
-            dot = sum_w<W>(dot);
             const float zr = zc * r.lse * r.inv;
 #pragma unroll
             for (int i = 0; i < C * V; ++i) {
