@@ -451,7 +451,9 @@ size_t coli_moe_project_workspace_bytes(const coli_moe_layer_t *layer, int32_t m
  *  x [T*K] bf16, T in [1, 65536];  y [T*N] bf16 (round-to-nearest-even) or
  *  fp32 (y_dtype); both 16-byte aligned and not overlapping.
  * Every row of y is written; rows of no request and requests without an
- * adapter get the projection alone.  The weights enter exactly (w = q*s),
+ * adapter get the projection alone.  A row of x, or an adapter, with NaN or
+ * infinities (or |x| of 2^110 and more) gives results that are not finite in
+ * its own rows; other rows and other adapters' gradients are not touched.  The weights enter exactly (w = q*s),
  * sums are fp32.  All three weight formats. */
 int coli_moe_project(const coli_moe_layer_t *layer, int32_t expert, int32_t matrix,
                      const coli_moe_adapters_t *adapters, const coli_moe_requests_t *requests,

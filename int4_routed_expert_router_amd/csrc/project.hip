@@ -351,7 +351,8 @@ COLI_DEV void shrink_tile(const ShrinkArgs &g, int tile, int sub, int split, f32
         for (int j = 0; j < 4; ++j) {
           const int t = t0 + 4 * kg + j;
           if (t >= begin && t < end && 16 * r + c < g.R32)
-            g.part[((int64_t)split * g.T + t) * g.R32 + 16 * r + c] = s * acc[r][j];
+            g.part[((int64_t)split * g.T + t) * g.R32 + 16 * r + c] =
+                16 * r + c < rank ? s * acc[r][j] : 0.0f;  // also for rows that are not finite
         }
     }
   });
@@ -514,7 +515,9 @@ COLI_DEV void load_b(const ExpandArgs &g, int a, int n0, int k, int rank, uint4 
 
 // acc += the adapters' part of the wavefront's MI x NJ tiles: rows t0 + 16i +
 // c, columns n0 + NJ c + j.  Every request with rows here multiplies only the
-// 16-row tiles that it reaches, its other rows as zeros.
+// 16-row tiles that it reaches.  Other requests' rows in a tile are multiplied
+// as zeros and keep their sums: a zero times an infinity or NaN of b would not
+// be zero.
 template <int MI, int NJ, int P>
 COLI_DEV void expand(const ExpandArgs &g, int t0, int n0, f32x4 (&acc)[MI][NJ]) {
   const int lane = threadIdx.x & 63, c = lane & 15, kg = lane >> 4;
@@ -532,10 +535,20 @@ COLI_DEV void expand(const ExpandArgs &g, int t0, int n0, f32x4 (&acc)[MI][NJ]) 
         const int t = t0 + 16 * i + c;
         uint4 uf[P];
         load_u<P>(g, t, k, t >= begin && t < end && k < rank, uf);
+        f32x4 d[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) d[j] = acc[i][j];
 #pragma unroll
         for (int p = 0; p < P; ++p)
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) acc[i][j] = mfma(uf[p], bf[j], acc[i][j]);
+          for (int j = 0; j < NJ; ++j) d[j] = mfma(uf[p], bf[j], d[j]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = t0 + 16 * i + 4 * kg + e;
+          const bool own = row >= begin && row < end;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) acc[i][j][e] = own ? d[j][e] : acc[i][j][e];
+        }
       }
     }
   });
@@ -601,9 +614,10 @@ struct GemmArgs {
 // with scales, and 201 us with five requests' rank-64 adapters (51 % busy; 2.5
 // times the vector instructions).  Steps on the way, on the plane: 201 us at
 // first, conflict-free reads 183 us, the third buffer 181 us, copies spread
-// between the matrix-core steps 164 us.  A 256 x
-// 256 tile has no registers left for the operands of the next stage.  w's rows are kept in the order n = 4c + j,
-// so that lane c ends up with four neighbouring columns, stored together.
+// between the matrix-core steps 164 us.  A 256 x 256 tile has no registers
+// left for the operands of the next stage.  w's rows are kept in the order n =
+// 4c + j, so that lane c ends up with four neighbouring columns, stored
+// together.
 template <int BM, int BN, int WM, bool SCALED, bool F32>
 __global__ void __launch_bounds__(BM / WM * BN) gemm_kernel(GemmArgs g) {
   constexpr int NW = (BM / WM) * (BN / 64), MI = WM / 16;
@@ -1367,7 +1381,7 @@ struct GradArgs {
 };
 struct GradsArgs {
   GradArgs g[2];  // dB (dy, u), dA (x, v)
-  const int32_t *owner;
+  const int32_t *owner, *rank;
   int T, Tp, R, R32, n, splits, rows;  // rows per split, a multiple of 64
 };
 
@@ -1452,10 +1466,16 @@ __global__ void __launch_bounds__(256) grads_kernel(GradsArgs a) {
   wave_sums<RT * 8, 4>(&acc[0][0], buf, wv, lane);
   if (wv != 0 || !cols) return;
   float *out = g.out + ((int64_t)split * a.n + ad) * a.R * g.F;
+  const int rank = rank_of(a.rank, ad, a.R);
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     const int rr = r0 + 16 * r + 4 * kg;  // four ranks; R is a multiple of 8
     if (rr >= a.R) continue;
+    // past the rank: zeros, also from rows that are not finite
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[r][j][e] = rr + e < rank ? acc[r][j][e] : 0.0f;
     if (g.transposed) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -1869,6 +1889,7 @@ int launch_project_backward(const Layer &L, int expert, int matrix, const coli_m
     a.g[0] = {dy, w.planes_u, w.sg > 1 ? w.pb : d_b, m.N, 1, (m.N + 127) / 128};
     a.g[1] = {x, w.planes_v, w.sg > 1 ? w.pa : d_a, m.K, 0, (m.K + 127) / 128};
     a.owner = w.owner;
+    a.rank = ad->rank;
     a.T = T;
     a.Tp = w.Tp;
     a.R = R;

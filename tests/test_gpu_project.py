@@ -218,6 +218,31 @@ def test_other_rows_do_not_leak():
     assert np.isnan(got[0][bad]).all()
 
 
+@pytest.mark.parametrize("T,H,I,fmt", [(60, 256, 128, "int4"), (60, 4160, 128, "int4"),
+                                       (300, 256, 128, "int8"), (1100, 512, 4096, "int4"),
+                                       (1100, 512, 4096, "mxfp4"), (1100, 4096, 512, "int8")])
+def test_broken_adapters_and_rows_stay_alone(T, H, I, fmt):
+    """An adapter full of NaN and infinities, and a row that is not finite,
+    leave the rows of other requests in the same tiles and other adapters'
+    gradients as they are; gradients past a rank stay zero."""
+    low = tu.Low(3, 16, I, H, ranks=(13, 16, 5))
+    off, who = [0, 3, 10, 21, 22, 37, T - 5], [0, 1, 2, 1, 0, 2]
+    c = Case(_spec(fmt, H, I), 0, T, off, who, low)
+    ref = [tu.host(t) for t in (c.forward(), c.forward(False), *c.backward())]
+    low.a[1], low.b[1] = float("nan"), float("inf")
+    c.ad = low.device()
+    c.x[37], c.dy[37] = float("inf"), float("inf")  # request 5's first row, adapter 2
+    got = [tu.host(t) for t in (c.forward(), c.forward(False), *c.backward())]
+    own = c.own.copy()
+    own[37] = 1
+    ok = own != 1
+    for g, r in zip(got[:3], ref[:3]):
+        assert np.array_equal(g[ok], r[ok])
+        assert not np.isfinite(g[own == 1]).any()
+    assert np.array_equal(got[3][0], ref[3][0]) and np.array_equal(got[4][0], ref[4][0])
+    assert not got[3][2, 5:].any() and not got[4][2, :, 5:].any()
+
+
 def test_rows_do_not_depend_on_their_batch():
     """Same bits twice, and outputs wanted one at a time are the same bits."""
     low = tu.Low(2, 16, 128, 256)
