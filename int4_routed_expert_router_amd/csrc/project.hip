@@ -611,7 +611,7 @@ struct GemmArgs {
 // (one fp32 FMA per output and 64-wide group): 8192 x 2048 x 6144 takes 164 to
 // 168 us on a plane of weights (1240 TFLOP/s, matrix cores busy in 65 % of the
 // cycles; the library's bf16 product of that size 153 us), 188 us on codes
-// with scales, and 201 us with five requests' rank-64 adapters (51 % busy; 2.5
+// with scales, and 201 to 210 us with five requests' rank-64 adapters (51 % busy; 2.5
 // times the vector instructions).  Steps on the way, on the plane: 201 us at
 // first, conflict-free reads 183 us, the third buffer 181 us, copies spread
 // between the matrix-core steps 164 us.  A 256 x 256 tile has no registers
@@ -1006,7 +1006,8 @@ __global__ void __launch_bounds__(64 * kStreamWaves) stream_kernel(StreamArgs g)
 // workgroup's four wavefronts, 64 rows x 32 columns each.  Otherwise as the
 // streaming path: parts and u first, joined by the second launch.  Bound by
 // the latency of a stage (0.8 us per 64 k with one stage in flight), which the
-// splits along K spread: 517 rows, 2048 x 1024 int4, 37 requests 25 us.
+// splits along K spread: 517 rows, 2048 x 1024 int4, 37 requests 17 us, the second
+// launch 9 us.
 constexpr int kDirectM = 4, kDirectN = 2, kDirectWaves = 4, kDirectGroups = 2;
 constexpr int kDirectRows = 16 * kDirectM, kDirectCols = 16 * kDirectN * kDirectWaves;
 
@@ -1209,7 +1210,7 @@ __global__ void __launch_bounds__(256) combine_parts_kernel(CombineArgs g) {
   combine_tile<F32>(g, blockIdx.x, blockIdx.y, blockIdx.z);
 }
 
-// The same for batches of mostly one-row requests (decode): a wavefront takes
+// The same for short requests, decode's single rows above all: a wavefront takes
 // 64 columns of one row, with plain fp32 products instead of matrix-core tiles
 // of which one row would be used.  B's rows come in whole cache lines (P lanes
 // to a row of at most P chunks of eight ranks, 64 / P rows per load), and
@@ -1657,6 +1658,17 @@ size_t carve(const Layer &L, int matrix, int n, int R, int T, bool backward, voi
   return c.used;
 }
 
+// Whether the second launch goes row by row (its cost: rows times rank) or by
+// tiles (tiles times the requests in each).  us by tiles / by rows:
+//   256 rows, rank  64,  4 rows per request: 13.0 /  9.8    8: 10.3 /  9.6
+//   517 rows, rank  64, 14 rows per request: 11.3 / 13.2
+//   517 rows, rank  24,  4 rows per request: 14.9 / 10.4   14: 10.2 /  8.9   21: 10.3 / 9.2
+//    64 rows, rank  16, 16 rows per request:  5.9 /  4.7
+//   512 rows, rank 128,  3 rows per request: 23.0 / 22.0    8: 35.2 / 53.0
+bool row_wise(int T, int n_req, int R) {
+  return T <= (int64_t)n_req * (R <= 64 ? 512 / (R < 16 ? 16 : R) : 2);
+}
+
 // Workgroups (per tile) that the requests of a tile are spread over.
 int spread(int rows, int n_req) { return n_req < rows ? n_req : rows; }
 // The same for the long requests' 64-row tiles: what a tile holds on average,
@@ -1786,7 +1798,7 @@ int launch_project(const Layer &L, int expert, int matrix, const coli_moe_adapte
                     : (fmt == kI8 ? launch_stream_rank<kI8>(g, m.N, w.R32, s)
                                   : launch_stream_rank<kF4>(g, m.N, w.R32, s));
     if (rc) return rc;
-    if (ad && 2 * (int64_t)e.q.n >= T) {
+    if (ad && row_wise(T, e.q.n, e.R)) {
       const dim3 rows((m.N + 255) / 256, T);
       if (f32) launch_k(COLI_K_PROJECT_COMBINE, combine_rows_kernel<true>, rows, dim3(256), 0, s, c);
       else launch_k(COLI_K_PROJECT_COMBINE, combine_rows_kernel<false>, rows, dim3(256), 0, s, c);

@@ -218,6 +218,18 @@ def test_other_rows_do_not_leak():
     assert np.isnan(got[0][bad]).all()
 
 
+@pytest.mark.parametrize("R", [8, 24, 40, 64, 72, 128])
+@pytest.mark.parametrize("rows", [1, 2, 3, 7, 9, 21, 33])
+def test_request_lengths_and_ranks(R, rows):
+    """Requests of a few rows each, at ranks on both sides of where the second
+    launch goes row by row; the tables of offsets below and above 64 entries."""
+    n = max(2, 100 // rows)
+    off = [rows * i for i in range(n + 1)]
+    low = tu.Low(5, R, 128, 192, ranks=(R, 1, max(1, R - 3), R, R // 2))
+    Case(_spec("int4", 192, 128), 0, rows * n + 3, off, [(3 * i) % 6 - 1 for i in range(n)],
+         low).check_forward()
+
+
 @pytest.mark.parametrize("T,H,I,fmt", [(60, 256, 128, "int4"), (60, 4160, 128, "int4"),
                                        (300, 256, 128, "int8"), (1100, 512, 4096, "int4"),
                                        (1100, 512, 4096, "mxfp4"), (1100, 4096, 512, "int8")])
