@@ -29,6 +29,7 @@
 //  finish   sums the parts of u and v and lays them out for
 //  grads    dA and dB, contractions over the rows of one adapter, split into
 //           row ranges that reduce adds up.
+#include "copy_ring.h"
 #include "internal.h"
 #include "spans.h"
 
@@ -622,7 +623,10 @@ template <int BM, int BN, int WM, bool SCALED, bool F32>
 __global__ void __launch_bounds__(BM / WM * BN) gemm_kernel(GemmArgs g) {
   constexpr int NW = (BM / WM) * (BN / 64), MI = WM / 16;
   constexpr int LD = (BM + BN) / 8 / NW;  // DMA instructions of a wavefront per stage
-  constexpr int VM = LD + (SCALED ? 1 : 0);
+  // operations of a wavefront that may be in flight: before the first stages are
+  // read the third one's copies, in a step those and the scale load before them
+  constexpr int kFirst = LD, VM = LD + (SCALED ? 1 : 0);
+  static_assert(ring_waits_hold(LD, SCALED, kFirst, VM) && VM < 16, "waits of the ring");
   // three objects, so that the compiler sees that one is read while others fill
   __shared__ uint4 stage0[(BM + BN) * 8], stage1[(BM + BN) * 8], stage2[(BM + BN) * 8];
   const int lane = threadIdx.x & 63, c = lane & 15, kg = lane >> 4;
@@ -757,7 +761,9 @@ __global__ void __launch_bounds__(BM / WM * BN) gemm_kernel(GemmArgs g) {
   }
   issue(stage1, 1);
   issue(stage2, 2);
-  __builtin_amdgcn_s_waitcnt(0x0F70 | (2 * LD & 15) | (2 * LD >> 4 << 14));
+  // stages 0 and 1: no scale load follows stage 1's copies, so the first step's
+  // wait alone would let its last copy be in flight
+  __builtin_amdgcn_s_waitcnt(0x0F70 | kFirst);
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < MI; ++i) read_a(stage0, i);
