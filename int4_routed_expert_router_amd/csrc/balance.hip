@@ -125,6 +125,10 @@ COLI_DEV float score(const Sig &g, float m, float e1) {
   return !SIGMOID ? e1 : (m >= 0.0f ? g.s : e1 * g.r);
 }
 
+// Rows whose largest logit is within this of zero take one exponential per
+// expert for sigmoid and softmax, others two.
+constexpr float kOneExp = 20.0f;
+
 // A row's probabilities p, exponentials e1 = exp(l - m), sigmoid complements
 // and log-sum-exp.  A row without a finite logit has p = e1 = 0 and lse = 0.
 template <int N>
@@ -142,10 +146,13 @@ COLI_DEV void row_probs(const float (&l)[N], Row<N> &o, const float *f = nullptr
   m = max_w<W>(m);
   const bool any = m > -INFINITY;
   float s = 0.0f, z = 0.0f;
-  if (SIGMOID && fabsf(m) <= 80.0f) {
-    // one exponential for both: e^l stays in range (the largest is e^80, and
-    // what underflows below is nothing beside the row's largest), and 1 /
-    // (1 + e^l) and e^l / (1 + e^l) are exact to a few steps
+  if (SIGMOID && fabsf(m) <= kOneExp) {
+    // one exponential for both, as 1 / (1 + e^l) and e^l / (1 + e^l) are exact
+    // to a few steps.  The hardware exponential gives 0 below 2^-126, for l <
+    // -87.3: at a largest logit of -kOneExp or more that is less than e^-67
+    // of it (nearer to -87 it would be seen: 255 experts 8.5 below a largest
+    // one of -79.5 are 5 % of their row).  e^l e^-m is off by (|l| + |m|)
+    // 2^-24, up to 2 kOneExp more than e^(l - m).
     const float em = __expf(-m);
 #pragma unroll
     for (int i = 0; i < N; ++i) {

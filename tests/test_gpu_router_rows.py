@@ -1,0 +1,47 @@
+"""Rows of the balance loss and the route's gradient at the edges of fp32's
+exponentials, against float64 (tests/train_util.py; tolerances as in
+test_gpu_balance.py): probabilities, losses and gradients of rows whose
+largest logit is given."""
+import numpy as np
+import pytest
+import torch
+
+import int4_routed_expert_router_amd as coli
+import train_util as tu
+from test_gpu_balance import E24, _check, _grad_scale, _layer, _run
+
+pytestmark = pytest.mark.gpu
+
+
+def _rows(T, E, k, top, seed=0):
+    """Logits of a spread of about 17 below a largest one of `top`."""
+    g = torch.Generator().manual_seed(seed)
+    l = torch.randn(T, E, generator=g) * 3
+    l = l - l.amax(dim=1, keepdim=True) + top
+    return l, l.topk(k, dim=1).indices.to(torch.int32)
+
+
+@pytest.mark.parametrize("sig", [False, True])
+@pytest.mark.parametrize("top", [-88.0, -80.5, -79.5, -76.0, -72.0, -60.0, -20.5, -19.5, 0.0, 19.5,
+                                 20.5, 60.0, 79.5, 80.5])
+def test_rows_by_their_largest_logit(top, sig):
+    T, E, k = 70, 256, 8
+    print("largest logit", top, sig, flush=True)
+    l, idx = _rows(T, E, k, top)
+    lh, ih = tu.host(l), idx.numpy().astype(np.int64)
+    dw, d_loss = torch.randn(T, k, generator=torch.Generator().manual_seed(1)), torch.tensor([0.7, -0.3])
+    D = np.max(np.max(lh, axis=1) - np.min(lh, axis=1))
+    for renorm in (False, True):
+        L = _layer(E, k, sig, renorm)
+        b = _run(L, l, idx, T)
+        _check(L, l, idx, None, None, sig, b)
+        bal = ([0, T], None, b.counts.cpu().numpy(), b.tokens.cpu().numpy())
+        for use_w, use_b in ((True, True), (True, False), (False, True)):
+            dl = torch.full((T, E), float("nan"), device="cuda")
+            coli.coli_moe_route_backward(L, l.cuda(), idx.cuda(), T, dw.cuda() if use_w else None,
+                                         b if use_b else None, d_loss.cuda() if use_b else None, dl)
+            args = (sig, renorm, 1.0, tu.host(dw) if use_w else None, bal if use_b else None,
+                    d_loss.double().numpy())
+            ref, S = tu.route_backward(lh, ih, *args), _grad_scale(lh, ih, *args)
+            bad = ~(np.abs(tu.host(dl) - ref) <= (4 * D + 2 * E + 64) * E24 * S + 1e-35)
+            assert not bad.any(), (renorm, use_w, use_b, np.argwhere(bad)[:4])
