@@ -529,8 +529,9 @@ int coli_moe_balance_loss(const coli_moe_layer_t *layer, const float *logits,
  *  filled for these logits) and d_loss [2] fp32, device: both given or both
  *  NULL.  At least one of the two parts is given.
  *  d_logits [T*E] fp32, every row written; with a balance, rows that do not
- *  count get zeros (their d_topk_w is not read).  d_logits does not
- *  overlap the inputs. */
+ *  count get zeros (their d_topk_w is not read), and so does a row of -inf
+ *  alone, which coli_moe_route, for finite logits, gives no weights.
+ *  d_logits does not overlap the inputs. */
 int coli_moe_route_backward(const coli_moe_layer_t *layer, const float *logits,
                             const int32_t *topk_idx, int32_t T, const float *d_topk_w,
                             const coli_moe_balance_t *balance, const float *d_loss,

@@ -529,7 +529,8 @@ COLI_DEV float route_part(const Chosen<KL> &ch, const float (&l)[KL], float c, f
         const Sig s = sigmoid(l[i]);
         d *= s.s * s.c;
       } else {
-        d *= __expf(l[i] - m) * inv;
+        // a row of -inf alone has no probabilities, and -inf - -inf no value
+        d = m > -INFINITY ? d * (__expf(l[i] - m) * inv) : 0.0f;
         out += d;
       }
       atomicAdd(&row[ch.e[i]], d);

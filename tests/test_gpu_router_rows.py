@@ -45,3 +45,31 @@ def test_rows_by_their_largest_logit(top, sig):
             ref, S = tu.route_backward(lh, ih, *args), _grad_scale(lh, ih, *args)
             bad = ~(np.abs(tu.host(dl) - ref) <= (4 * D + 2 * E + 64) * E24 * S + 1e-35)
             assert not bad.any(), (renorm, use_w, use_b, np.argwhere(bad)[:4])
+
+
+@pytest.mark.parametrize("E,k", [(8, 2), (64, 8), (256, 8), (7, 3), (1024, 32)])
+@pytest.mark.parametrize("sig", [False, True])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_rows_without_a_finite_logit(E, k, sig, renorm):
+    """A counted row of -inf alone has no probabilities: its gradients are
+    zero, also those of its routing weights, and other rows keep their bits."""
+    T, gone = 37, [0, 5, 6, 36]
+    print("rows of -inf", E, k, sig, renorm, flush=True)
+    L = _layer(E, k, sig, renorm, 2.5)
+    g = torch.Generator().manual_seed(E)
+    l = torch.randn(T, E, generator=g)
+    idx = l.topk(k, dim=1).indices.to(torch.int32)
+    dw, d_loss = torch.randn(T, k, generator=g), torch.tensor([0.7, -0.3])
+    b = _run(L, l, idx, T)  # the counts are inputs here, and the same for both
+    rest = np.setdiff1d(np.arange(T), gone)
+    for use_w, use_b in ((True, True), (True, False), (False, True)):
+        got = []
+        for rows in ([], gone):
+            x = l.clone()
+            x[rows] = float("-inf")
+            dl = torch.full((T, E), float("nan"), device="cuda")
+            coli.coli_moe_route_backward(L, x.cuda(), idx.cuda(), T, dw.cuda() if use_w else None,
+                                         b if use_b else None, d_loss.cuda() if use_b else None, dl)
+            got.append(tu.host(dl))
+        assert np.array_equal(got[1][gone], np.zeros((len(gone), E))), (use_w, use_b)
+        assert np.array_equal(got[1][rest], got[0][rest]), (use_w, use_b)
