@@ -37,8 +37,13 @@ namespace {
 constexpr int kFwdThreads = 512;
 constexpr int kMaxTiles = 512;
 constexpr int kMaxFinish = 512;  // workgroups of the second kernel
-constexpr int kSoloRows = 64;    // up to here one workgroup does everything
 constexpr int kCols = 16;        // experts per item of the second kernel
+// One workgroup does everything for few rows and few items (sequences times
+// kCols experts), which it takes one after another, 0.6 us each.  us by one
+// launch / two, 40 rows (4 and 64 rows alike):
+//   1 item  6.8 / 9.3   4: 7.5 / 10.0   8: 11.1 / 11.4   16: 15.3 / 10.1
+//   64 items 44 / 13   1,024: 579 / 26   4,800: 2,519 / 30
+constexpr int kSoloRows = 64, kSoloItems = 8;
 
 // Reductions over aligned groups of W lanes, the result in every lane: DPP
 // moves within 16 lanes (neighbours, pairs, mirrored halves, mirrored row),
@@ -695,7 +700,8 @@ __global__ void __launch_bounds__(kBwdThreads) route_backward_kernel(BwdArgs g) 
 template <int W, int C, int V, bool SIGMOID>
 int launch_fwd(FwdArgs g, hipStream_t s) {
   constexpr int G = kFwdThreads / W;
-  if (g.T <= kSoloRows) {
+  const int64_t items = (int64_t)g.n_seq * ((g.E + kCols - 1) / kCols);
+  if (g.T <= kSoloRows && items <= kSoloItems) {
     g.tile = kSoloRows;
     g.n_tiles = 1;
     launch_k(COLI_K_BALANCE, balance_kernel<W, C, V, SIGMOID, true>, dim3(1), dim3(kFwdThreads), 0,
@@ -706,7 +712,6 @@ int launch_fwd(FwdArgs g, hipStream_t s) {
   g.n_tiles = (g.T + g.tile - 1) / g.tile;
   launch_k(COLI_K_BALANCE, balance_kernel<W, C, V, SIGMOID, false>, dim3(g.n_tiles),
            dim3(kFwdThreads), 0, s, g);
-  const int64_t items = (int64_t)g.n_seq * ((g.E + kCols - 1) / kCols);
   launch_k(COLI_K_BALANCE_FINISH, balance_finish_kernel,
            dim3((unsigned)(items < kMaxFinish ? items : kMaxFinish)), dim3(kFwdThreads), 0, s, g);
   return hip_status(hipGetLastError());

@@ -8,7 +8,7 @@ import torch
 
 import int4_routed_expert_router_amd as coli
 import train_util as tu
-from test_gpu_balance import E24, _check, _grad_scale, _layer, _run
+from test_gpu_balance import E24, _check, _grad_scale, _inputs, _layer, _run
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +73,23 @@ def test_rows_without_a_finite_logit(E, k, sig, renorm):
             got.append(tu.host(dl))
         assert np.array_equal(got[1][gone], np.zeros((len(gone), E))), (use_w, use_b)
         assert np.array_equal(got[1][rest], got[0][rest]), (use_w, use_b)
+
+
+@pytest.mark.parametrize("E,k", [(8, 2), (256, 8)])
+@pytest.mark.parametrize("n_seq", [1, 2, 9, 40, 3000])
+def test_few_rows_in_many_sequences(E, k, n_seq):
+    """A padded table of sequences, most of them empty: results, and that a
+    single workgroup is left alone only with a few of them."""
+    T = 40
+    print("sequences", E, n_seq, flush=True)
+    inner = np.sort(np.random.default_rng(n_seq).integers(0, T + 1, n_seq - 1))
+    off = np.concatenate(([0], inner, [T])).tolist()
+    valid = (np.arange(T) % 7 != 1).astype(np.uint8)
+    l, idx = _inputs(T, E, k)
+    L = _layer(E, k, True)
+    _check(L, l, idx, off, valid, True, _run(L, l, idx, T, off, valid))
+    with coli.KernelTimer() as timer:
+        _run(L, l, idx, T, off, valid)
+    names = [n for n, _ in timer.results()]
+    timer.close()
+    assert names == (["balance", "balance_finish"] if n_seq * -(-E // 16) > 8 else ["balance"])
