@@ -849,10 +849,11 @@ COLI_DEV Raw<F> load_raw(const Matrix &m, int n, int b, int kg) {
   else r.s = reinterpret_cast<const uint16_t *>(m.sc)[(int64_t)n * (m.K / 64) + b];
   return r;
 }
-// Step h as a matrix-core operand.  int4: the bf16 value 24 + q (a nibble in
-// the mantissa of 16 .. 31), pairs (k, k + 4); the bias leaves through the
-// accumulator's start value, -24 times the row's sum of x.  int8: exact
-// values.  MXFP4: the weights themselves.
+// Step h as a matrix-core operand, exact in bf16.  int4: 16 q, a nibble in the
+// upper half of a signed byte (a biased form such as 24 + q takes half the
+// instructions, but its bias times sum(x) has to leave the fp32 sums again:
+// where large x meet small codes, little else than rounding stays).  int8: q.
+// MXFP4: the weights themselves.
 template <int F>
 COLI_DEV uint4 unpack(const Raw<F> &r, int h) {
   if (F == kBF) {
@@ -861,12 +862,12 @@ COLI_DEV uint4 unpack(const Raw<F> &r, int h) {
     return v;
   }
   if (F == kI4) {
-    const uint32_t w = r.w[h];
-    constexpr uint32_t M = 0x00780078u, X = 0x41c041c0u;
-    return make_uint4(__builtin_amdgcn_bitop3_b32(w << 3, M, X, kAndXor),
-                      __builtin_amdgcn_bitop3_b32(w >> 1, M, X, kAndXor),
-                      __builtin_amdgcn_bitop3_b32(w >> 5, M, X, kAndXor),
-                      __builtin_amdgcn_bitop3_b32(w >> 9, M, X, kAndXor));
+    const uint32_t w = r.w[h], even = (w << 4) & 0xf0f0f0f0u, odd = w & 0xf0f0f0f0u;
+    uint32_t d[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      d[i] = pack_bf16((float)(int8_t)(even >> (8 * i)), (float)(int8_t)(odd >> (8 * i)));
+    return make_uint4(d[0], d[1], d[2], d[3]);
   }
   if (F == kI8) {
     uint32_t d[4];
@@ -885,6 +886,13 @@ COLI_DEV uint4 unpack(const Raw<F> &r, int h) {
       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1)),
       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2)),
       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3)));
+}
+
+// What a group's sum of products with unpack's operands is multiplied by.
+template <int F>
+COLI_DEV float group_scale(const Raw<F> &r) {
+  const float s = f16_to_f32((uint16_t)r.s);
+  return F == kI4 ? s * 0.0625f : s;
 }
 
 // One workgroup: 16 MT rows x 16 NJ columns (n0 + NJ c + j) over one split of
@@ -922,30 +930,13 @@ COLI_DEV void stream_tile(const StreamArgs &g, int nt, int tt, int split, f32x4 
 #pragma unroll
     for (int i = 0; i < GB; ++i) {
       if (b + i >= b1) continue;
-      f32x4 start[MT];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        start[m] = f32x4{0, 0, 0, 0};
-        if (F == kI4) {
-          constexpr uint32_t kMinus24 = 0xc1c0c1c0u;
-          const uint4 ones = make_uint4(kMinus24, kMinus24, kMinus24, kMinus24);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t d[4] = {xr[i][m][h].x, xr[i][m][h].y, xr[i][m][h].z, xr[i][m][h].w};
-            uint32_t o[4];
-            x8_to_pairs(d, o);
-            xr[i][m][h] = make_uint4(o[0], o[1], o[2], o[3]);
-            start[m] = mfma(xr[i][m][h], ones, start[m]);
-          }
-        }
-      }
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         const uint4 w0 = unpack<F>(raw[i][j], 0), w1 = unpack<F>(raw[i][j], 1);
-        const float s = exact ? 1.0f : f16_to_f32((uint16_t)raw[i][j].s);
+        const float s = exact ? 1.0f : group_scale(raw[i][j]);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          f32x4 d = exact ? acc[m][j] : start[m];
+          f32x4 d = exact ? acc[m][j] : f32x4{0, 0, 0, 0};
           d = mfma(xr[i][m][0], w0, d);
           d = mfma(xr[i][m][1], w1, d);
           if (exact) {
@@ -1072,7 +1063,7 @@ COLI_DEV void direct_tile(const StreamArgs &g, int nt, int tt, int split, uint4 
       for (int j = 0; j < NJ; ++j) {
         w[s][j][0] = unpack<F>(raw[s][j], 0);
         w[s][j][1] = unpack<F>(raw[s][j], 1);
-        sc[s][j] = exact ? 1.0f : f16_to_f32((uint16_t)raw[s][j].s);
+        sc[s][j] = exact ? 1.0f : group_scale(raw[s][j]);
       }
     if (st + 1 < nst) issue(to, st + 1);
 #pragma unroll
@@ -1081,22 +1072,11 @@ COLI_DEV void direct_tile(const StreamArgs &g, int nt, int tt, int split, uint4 
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         uint4 af[2];
-        f32x4 start = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          af[h] = A[(16 * i + c) * RB + ((8 * s + 2 * kg + h) ^ key(c))];
-          if (F == kI4) {
-            constexpr uint32_t kMinus24 = 0xc1c0c1c0u;
-            const uint32_t d[4] = {af[h].x, af[h].y, af[h].z, af[h].w};
-            uint32_t o[4];
-            x8_to_pairs(d, o);
-            af[h] = make_uint4(o[0], o[1], o[2], o[3]);
-            start = mfma(af[h], make_uint4(kMinus24, kMinus24, kMinus24, kMinus24), start);
-          }
-        }
+        for (int h = 0; h < 2; ++h) af[h] = A[(16 * i + c) * RB + ((8 * s + 2 * kg + h) ^ key(c))];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-          f32x4 d = exact ? acc[i][j] : start;
+          f32x4 d = exact ? acc[i][j] : f32x4{0, 0, 0, 0};
           d = mfma(af[0], w[s][j][0], d);
           d = mfma(af[1], w[s][j][1], d);
           if (exact) {
