@@ -419,6 +419,9 @@ def _project_args(layer, matrix, adapters, requests, x, T):
     n, k = _shape_nk(layer, matrix)
     dev = x.get_device()
     _need(x, "x", torch.bfloat16, T * k, dev)
+    for w in (layer.q4, layer.scales):
+        if isinstance(w, torch.Tensor) and w.get_device() != dev:
+            raise ValueError("the layer's weights on %s, x on %s" % (w.device, x.device))
     if adapters is None or requests is None:
         ad = None if adapters is None else ctypes.byref(adapters.c)
         return n, k, dev, ad, None if requests is None else ctypes.byref(requests.c)
