@@ -453,8 +453,11 @@ size_t coli_moe_project_workspace_bytes(const coli_moe_layer_t *layer, int32_t m
  * Every row of y is written; rows of no request and requests without an
  * adapter get the projection alone.  A row of x, or an adapter, with NaN or
  * infinities (or |x| of 2^110 and more) gives results that are not finite in
- * its own rows; other rows and other adapters' gradients are not touched.  The weights enter exactly (w = q*s),
- * sums are fp32.  All three weight formats. */
+ * its own rows; other rows and other adapters' gradients are not touched.  The
+ * weights enter exactly (w = q*s), sums are fp32, in an order that depends on T:
+ * a row in a batch of another size may differ in its last bits.  All three
+ * weight formats; MXFP4 weights of 2^128 and more, which E8M0 bytes 253 and 254
+ * can stand for, are infinities. */
 int coli_moe_project(const coli_moe_layer_t *layer, int32_t expert, int32_t matrix,
                      const coli_moe_adapters_t *adapters, const coli_moe_requests_t *requests,
                      const uint16_t *x, int32_t T, void *y, int32_t y_dtype, void *ws,
@@ -470,7 +473,8 @@ int coli_moe_project(const coli_moe_layer_t *layer, int32_t expert, int32_t matr
  * d_a and d_b are both given or both NULL (and NULL without adapters).  They
  * are written whole, not added to: zeros for adapters that no row uses and
  * past an adapter's rank.  At least one output is given.  dx uses W rounded
- * to bf16. */
+ * to bf16, the type dx has itself (MXFP4 weights lose nothing by it); the same
+ * W for every T. */
 int coli_moe_project_backward(const coli_moe_layer_t *layer, int32_t expert, int32_t matrix,
                               const coli_moe_adapters_t *adapters,
                               const coli_moe_requests_t *requests, const uint16_t *x,
@@ -525,9 +529,13 @@ int coli_moe_balance_loss(const coli_moe_layer_t *layer, const float *logits,
  * where topk_w are the routing weights of coli_moe_route for this layer's
  * flags and routed_scale, the choice of experts and the counts being
  * constants.
- *  d_topk_w [T*k] fp32 or NULL;  balance (the buffers coli_moe_balance_loss
- *  filled for these logits) and d_loss [2] fp32, device: both given or both
- *  NULL.  At least one of the two parts is given.
+ *  d_topk_w [T*k] fp32 or NULL: for the layer's output y, dy[t] times the
+ *  output of expert topk_idx[t][j] for row t.  The caller brings it: the
+ *  forward calls add the experts' outputs up and return none of them alone
+ *  (coli_moe_project computes one expert's projections).
+ *  balance (the buffers coli_moe_balance_loss filled for these logits) and
+ *  d_loss [2] fp32, device: both given or both NULL.  At least one of the two
+ *  parts is given.
  *  d_logits [T*E] fp32, every row written; with a balance, rows that do not
  *  count get zeros (their d_topk_w is not read), and so does a row of -inf
  *  alone, which coli_moe_route, for finite logits, gives no weights.

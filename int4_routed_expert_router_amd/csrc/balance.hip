@@ -18,8 +18,8 @@
 // into a wavefront.  65,536 x 256 logits (67 MB): the loss 26 us (19 us for the
 // rows, 3.5 TB/s, and the second launch), the gradient of a sigmoid layer with
 // renormalised weights 38 us, 3.6 TB/s over read and write; its vector ALUs
-// issue in 69 % of the cycles (272 instructions per row).  With a second
-// exponential for the softmax, instead of e^l for both, it took 41 us.
+// issue in 68 % of the cycles (272 instructions per row).  Rows whose largest
+// logit is beyond kOneExp, with a second exponential, take 40 to 41.5 us.
 // Smaller batches are bound by latency: 5 to 7 us per launch.
 //
 // Sums over tokens take a fixed order (no floating-point atomics): a

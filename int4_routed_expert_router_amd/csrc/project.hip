@@ -14,7 +14,9 @@
 // uses w = q*s exactly: each 64-wide group's partial product is multiplied by
 // its scale in fp32.  W^T in dx is contracted across groups, where the scale
 // cannot be taken out of the sum: there w is rounded to bf16, half a step of
-// the type that dx itself is rounded to.  u and v stay fp32 and enter the
+// the type that dx itself is rounded to (MXFP4 weights are exact; a second part
+// of w would double the long batches' product, and dx uses the same W for
+// every T).  u and v stay fp32 and enter the
 // matrix cores as sums of two bf16 parts (16 bits of mantissa, for bf16
 // results) or three (24 bits, for fp32 ones).
 //
@@ -187,7 +189,7 @@ __global__ void __launch_bounds__(256) prep_kernel(Matrix m, uint16_t *plane, fl
   *reinterpret_cast<uint4 *>(plane + 8 * i) = make_uint4(d[0], d[1], d[2], d[3]);
 }
 
-// The backward pass's operands: the weights as bf16 [K][N], and A and B of
+// The backward pass's operands: the weights rounded to bf16 (see the top) [K][N], and A and B of
 // every adapter in use transposed to [K][R] and [R][N].  One 64 x 64 tile
 // per workgroup, through LDS.
 struct PrepT {
@@ -612,7 +614,7 @@ struct GemmArgs {
 // (one fp32 FMA per output and 64-wide group): 8192 x 2048 x 6144 takes 164 to
 // 168 us on a plane of weights (1240 TFLOP/s, matrix cores busy in 65 % of the
 // cycles; the library's bf16 product of that size 153 us), 188 us on codes
-// with scales, and 201 to 210 us with five requests' rank-64 adapters (51 % busy; 2.5
+// with scales, and 201 to 218 us with five requests' rank-64 adapters (51 % busy; 2.5
 // times the vector instructions).  Steps on the way, on the plane: 201 us at
 // first, conflict-free reads 183 us, the third buffer 181 us, copies spread
 // between the matrix-core steps 164 us.  A 256 x 256 tile has no registers
@@ -1528,9 +1530,10 @@ int shrink_splits(int T, int F) {
   if (s > F / 256) s = F / 256;
   return s < 1 ? 1 : (s > kMaxSplits ? kMaxSplits : s);
 }
-// Row ranges of the gradients: about 512 workgroups, two to a CU (8192 rows,
-// two adapters of rank 64, 6144 and 2048 columns: 26.8 us, against 37.8 us with
-// 1,024 and 32.8 us with 256).
+// Row ranges of the gradients: about 512 workgroups, which run in two rounds
+// (at rank 64 a wavefront takes 384 registers, so a CU holds one workgroup).
+// 8192 rows, two adapters of rank 64, 6144 and 2048 columns: 26.8 us, against
+// 37.8 us with 1,024 and 32.8 us with 256.
 int grad_splits(int T, int N, int K, int n) {
   const int64_t blocks = (int64_t)((N + 127) / 128 + (K + 127) / 128) * n;
   const int windows = (T + 255) / 256;  // a window per wavefront
@@ -1547,7 +1550,13 @@ int grad_splits(int T, int N, int K, int n) {
 // The streaming kernel reads x once per 16-64 columns, which pays only for
 // few rows (more of them where K is long and its splits keep the chip busy);
 // the gemm needs its 256 x 128 tiles to reach most CUs and a pass that
-// unpacks the weights.
+// unpacks the weights.  Narrow matrices (us, direct / gemm, 8 requests of
+// rank 32; the bound of 96 tiles is what wide ones need, and in between these
+// are on the slower side of it):
+//   N  128 K 2048, T 1024: 16 / 44   T 4096: 33 / 47   T 8192: 47 / 46   T 16384: 80 / 49
+//   N  512 K 2048, T 1024: 24 / 45   T 2048: 34 / 46   T 4096: 60 / 49
+//   N  512 K 6144, T 1024: 51 / 94   T 2048: 77 / 95   T 4096: 141 / 97
+//   N 1024 K 2048, T  600: 23 / 48   T 1024: 30 / 48   T 2048: 54 / 49
 enum Path { kStream, kDirect, kGemm };
 Path path_of(int T, int N, int K) {
   if (T <= (K > 4096 ? 128 : 32)) return kStream;
