@@ -545,6 +545,177 @@ int coli_moe_route_backward(const coli_moe_layer_t *layer, const float *logits,
                             const coli_moe_balance_t *balance, const float *d_loss,
                             float *d_logits, void *stream);
 
+/* ---- the norm in front of the layer -----------------------------------------
+ * hidden  H, a multiple of 8 in [8, 16384].
+ * eps     added to the mean of squares; finite and above zero.
+ * weight  [H] device, bf16 or fp32 (weight_dtype, a COLI_SRC_*), 16-byte
+ *         aligned; NULL: all ones.  */
+typedef struct coli_moe_norm {
+  int32_t hidden;
+  float eps;
+  const void *weight;
+  int32_t weight_dtype;
+} coli_moe_norm_t;
+
+/* codes that coli_moe_norm writes beside (or in place of) y */
+enum { COLI_NORM_PLAIN = 0, COLI_NORM_Q8_0 = 1, COLI_NORM_MXFP8 = 2 };
+
+/* Root-mean-square norm of T rows, with the residual's addition in front and
+ * the codes of the prefill path behind, in one pass:
+ *   s[t] = residual[t] + x[t], rounded to the stream's type (without a
+ *          residual s = x);  total[t] = s[t]
+ *   y[t] = s[t] / sqrt(mean over H of s[t]^2 + eps) * weight, rounded to bf16
+ *   q, scales = the codes of y, bit for bit those of coli_moe_quantize_q8_0
+ *          (COLI_NORM_Q8_0) or coli_moe_quantize_mxfp8 (COLI_NORM_MXFP8)
+ * The norm is that of the stored s, so that a backward pass and later layers,
+ * which see nothing else, agree with it; the codes are those of the bf16 y, so
+ * that router and experts see the same values.  Sums are fp32; the sum of a
+ * row's squares has to stay below 2^128.
+ *  x [T*H] bf16;  residual, total [T*H] of residual_dtype (COLI_SRC_BF16 or
+ *  _F32), both given or both NULL (total may be residual itself);
+ *  y [T*H] bf16 or NULL (may be x itself);  format a COLI_NORM_*: q [T*H]
+ *  bytes and scales [T*H/32] as the quantiser of that format writes them, both
+ *  NULL for COLI_NORM_PLAIN; codes need H a multiple of 32
+ *  (COLI_E_UNSUPPORTED).  At least one of y and q is given.  T in [1, 2^24].
+ *  All 16-byte aligned; scales 4-byte.  Other overlaps are not allowed.
+ * A row with NaN or infinities gives such a row, with codes that are not
+ * specified; other rows are not touched by it. */
+int coli_moe_norm(const coli_moe_norm_t *norm, const uint16_t *x, const void *residual,
+                  int32_t residual_dtype, int32_t T, void *total, uint16_t *y, int32_t format,
+                  void *q, void *scales, void *stream);
+
+/* Bytes of workspace of coli_moe_norm_backward for T rows when d_weight is
+ * asked for; it also does for fewer rows.  0 for invalid arguments.  Host-only. */
+size_t coli_moe_norm_workspace_bytes(const coli_moe_norm_t *norm, int32_t T);
+
+/* The backward pass of coli_moe_norm from total (or x, where there was no
+ * residual) and the gradient of y (for codes that of the y they stand for);
+ * nothing else is kept from the forward pass.  With r[t] = 1 / sqrt(mean s^2 +
+ * eps), h = s r and n = dy weight:
+ *   d[t] = r (n - h mean(n h)) + d_total[t]
+ *   d_weight = sum over t of dy[t] h[t]
+ * d is the gradient of x and of residual alike.
+ *  total, d_total [T*H] of total_dtype (COLI_SRC_*), dy [T*H] bf16; d_total,
+ *  the gradient that reaches the stream past this layer, may be NULL;
+ *  dx [T*H] bf16 or NULL (may be dy itself, or d_total of that type);
+ *  d_residual [T*H] of total_dtype or NULL (may be d_total itself; the same d
+ *  as dx, for a stream of another type);  d_weight [H] fp32 or NULL, written
+ *  whole.  At least one output is given.  T in [1, 2^24]; all 16-byte
+ *  aligned.  ws is read and written only for d_weight. */
+int coli_moe_norm_backward(const coli_moe_norm_t *norm, const void *total, int32_t total_dtype,
+                           const uint16_t *dy, const void *d_total, int32_t T, uint16_t *dx,
+                           void *d_residual, float *d_weight, void *ws, size_t ws_bytes,
+                           void *stream);
+
+/* coli_moe_forward_prefill of activations that are quantised already, as
+ * coli_moe_norm writes them: q [T*H] and scales [T*H/32] in MXFP8 for layers
+ * flagged COLI_ACT_MXFP8, else in Q8_0 (codes in [-127, 127]); both 16-byte
+ * aligned.  The same result, bit for bit, as coli_moe_forward_prefill of the
+ * bf16 values they were made from; same workspace and errors. */
+int coli_moe_forward_prefill_quantized(const coli_moe_layer_t *layer,
+                                       const coli_moe_route_t *route, const void *q,
+                                       const void *scales, int32_t T, void *y, int32_t y_dtype,
+                                       void *ws, size_t ws_bytes, void *stream);
+
+/* ---- a batch's rows sorted by expert, and back ------------------------------
+ * For products that are computed expert by expert (coli_moe_project on each
+ * expert's rows) instead of in one forward call, and for their gradients.
+ * Pair p = t*k + j, token t's j-th choice, owns row route->pair_pos[p] of a
+ * buffer of n_rows rows of H values.  coli_moe_route writes the order that
+ * makes every expert's rows adjacent (n_rows = T*k; expert e's rows are
+ * offsets[e] .. offsets[e+1]).  A caller may write others: a pair whose
+ * pair_pos is outside [0, n_rows) has no row (it went over an expert's limit,
+ * or its expert is on another device); the rows of different pairs have to be
+ * different.  Rows that no pair owns are neither read nor written.
+ * These calls read route->pair_pos and, where stated, route->topk_w, and H, E
+ * and k of `layer` (no weights).  T in [1, 65536], T*k <= 2^20, n_rows in
+ * [1, 2^21].  Element types are COLI_SRC_BF16 or COLI_SRC_F32; sums are fp32,
+ * in the order of j, rounded once.  All [..*H] buffers 16-byte aligned, and
+ * not overlapping except where stated. */
+
+/* rows[pair_pos[t*k + j]] = x[t] for every pair that has a row.
+ *  x [T*H], rows [n_rows*H], both of `dtype`. */
+int coli_moe_dispatch(const coli_moe_layer_t *layer, const coli_moe_route_t *route, const void *x,
+                      int32_t dtype, int32_t T, void *rows, int64_t n_rows, void *stream);
+
+/* The gradient of coli_moe_dispatch: dx[t] = sum_j d_rows[pair_pos[t*k + j]]
+ * (+ beside[t]: gradients that reach x past the rows, e.g. from the shared
+ * expert; NULL: none), over the pairs that have a row.
+ *  d_rows [n_rows*H] and beside [T*H] of rows_dtype;  dx [T*H] of dx_dtype
+ *  (may be beside itself if the types agree). */
+int coli_moe_dispatch_backward(const coli_moe_layer_t *layer, const coli_moe_route_t *route,
+                               const void *d_rows, int32_t rows_dtype, int64_t n_rows,
+                               const void *beside, int32_t T, void *dx, int32_t dx_dtype,
+                               void *stream);
+
+/* y[t] = sum_j topk_w[t*k + j] rows[pair_pos[t*k + j]] (+ beside[t]: the shared
+ * expert's output; NULL: none), over the pairs that have a row.
+ *  rows [n_rows*H] and beside [T*H] of rows_dtype;  y [T*H] of y_dtype (may be
+ *  beside itself if the types agree). */
+int coli_moe_combine(const coli_moe_layer_t *layer, const coli_moe_route_t *route,
+                     const void *rows, int32_t rows_dtype, int64_t n_rows, const void *beside,
+                     int32_t T, void *y, int32_t y_dtype, void *stream);
+
+/* The gradients of coli_moe_combine from rows and the gradient dy of y (which
+ * is that of beside too):
+ *   d_rows[pair_pos[p]] = topk_w[p] dy[t]       for every pair that has a row
+ *   d_topk_w[p] = sum over H of dy[t] rows[pair_pos[p]], or 0 without a row
+ * d_topk_w is what coli_moe_route_backward takes.
+ *  rows, d_rows [n_rows*H] of rows_dtype (d_rows may be rows itself);  dy
+ *  [T*H] of dy_dtype;  d_topk_w [T*k] fp32.  d_rows or d_topk_w may be NULL,
+ *  not both; rows may be NULL without d_topk_w. */
+int coli_moe_combine_backward(const coli_moe_layer_t *layer, const coli_moe_route_t *route,
+                              const void *rows, int32_t rows_dtype, int64_t n_rows,
+                              const void *dy, int32_t dy_dtype, int32_t T, void *d_rows,
+                              float *d_topk_w, void *stream);
+
+/* ---- clipping by the global gradient norm -----------------------------------
+ * One gradient and where its clipped values go; host memory.
+ *  grad, out : device, n values each of their COLI_SRC_* types, aligned to the
+ *              type.  out may be grad itself (same type); otherwise no out may
+ *              overlap another out or any grad.  n in [0, 2^40]. */
+typedef struct coli_moe_gradient {
+  const void *grad;
+  void *out;
+  int64_t n;
+  int32_t grad_dtype;
+  int32_t out_dtype;
+} coli_moe_gradient_t;
+
+/* A piece of a gradient, as the kernels take them. */
+typedef struct coli_moe_clip_item {
+  const void *grad;
+  void *out;
+  int32_t n;
+  int32_t dtypes; /* bit 0: grad is fp32, bit 1: out is fp32 */
+  int64_t order;
+} coli_moe_clip_item_t;
+
+/* Plans a clipping of n gradients (n in [0, 2^20]) on the host: the number of
+ * pieces, and the pieces themselves, which the caller copies to the device and
+ * uses for as many calls as the gradients stay where they are.
+ * coli_moe_clip_items returns a negative COLI_E_* code for gradients that are
+ * not valid; coli_moe_clip_plan writes exactly that many items. Host-only. */
+int64_t coli_moe_clip_items(const coli_moe_gradient_t *gradients, int32_t n);
+int coli_moe_clip_plan(const coli_moe_gradient_t *gradients, int32_t n,
+                       coli_moe_clip_item_t *items, int64_t n_items);
+
+/* Bytes of workspace of coli_moe_clip_gradients, the same for every plan. */
+size_t coli_moe_clip_workspace_bytes(void);
+
+/* The norm over all gradients of a plan, and clipping:
+ *   norm[0] = sqrt(sum of all squares), the sum in 64 bits: no square
+ *             overflows or vanishes
+ *   norm[1] = max_norm / norm[0] where norm[0] > max_norm, else 1; 1 also where
+ *             norm[0] is NaN or infinite, which the caller has to look for
+ *   out = grad * norm[1], rounded to out's type
+ * An out that is its grad is not touched where norm[1] is 1.
+ *  items [n_items] device, 8-byte aligned, from coli_moe_clip_plan (n_items
+ *  may be 0: norm 0);  max_norm >= 0, infinity for the norm alone;  norm [2]
+ *  fp32, device. */
+int coli_moe_clip_gradients(const coli_moe_clip_item_t *items, int64_t n_items, float max_norm,
+                            float *norm, void *ws, size_t ws_bytes, void *stream);
+
 /* ---- optional kernel timing ----------------------------------------------
  * For benchmarks and profilers.  After coli_moe_set_trace(t) with t != NULL,
  * every later launch hands t->start[i] and t->stop[i] to the dispatch of its
@@ -566,7 +737,9 @@ enum {
   COLI_K_ROUTE_BACKWARD = 19, COLI_K_PROJECT_PREP = 20, COLI_K_PROJECT_SHRINK = 21,
   COLI_K_PROJECT_GEMM = 22, COLI_K_PROJECT_FINISH = 23, COLI_K_PROJECT_GRADS = 24,
   COLI_K_PROJECT_REDUCE = 25, COLI_K_PROJECT_STREAM = 26, COLI_K_PROJECT_COMBINE = 27,
-  COLI_K_COUNT = 28
+  COLI_K_NORM = 28, COLI_K_NORM_BACKWARD = 29, COLI_K_NORM_REDUCE = 30, COLI_K_DISPATCH = 31,
+  COLI_K_ROWS_COMBINE = 32, COLI_K_ROWS_BACKWARD = 33, COLI_K_CLIP_NORM = 34,
+  COLI_K_CLIP_SCALE = 35, COLI_K_COUNT = 36
 };
 typedef struct coli_moe_trace {
   void **start;     /* hipEvent_t[capacity] */

@@ -17,6 +17,7 @@ COLI_SRC_BF16, COLI_SRC_F32 = 0, 1
 COLI_ENTRY_ROUTE, COLI_ENTRY_DECODE, COLI_ENTRY_PREFILL = 0, 1, 2
 COLI_WEIGHTS_INT4, COLI_WEIGHTS_INT8, COLI_WEIGHTS_MXFP4 = 0, 1, 2
 COLI_ACT_MXFP8 = 1 << 16
+COLI_NORM_PLAIN, COLI_NORM_Q8_0, COLI_NORM_MXFP8 = 0, 1, 2
 
 
 class ColiError(RuntimeError):
@@ -47,7 +48,9 @@ KERNEL_NAMES = ["route_fused", "route_topk", "route_group", "decode_gateup", "de
                 "router_logits", "quantize_int4", "quantize_int8", "quantize_mxfp4", "read_probe",
                 "mfma_probe", "balance", "balance_finish", "route_backward", "project_prep",
                 "project_shrink", "project_gemm", "project_finish", "project_grads",
-                "project_reduce", "project_stream", "project_combine"]
+                "project_reduce", "project_stream", "project_combine", "norm", "norm_backward",
+                "norm_reduce", "dispatch", "rows_combine", "rows_backward", "clip_norm",
+                "clip_scale"]
 
 
 class _RouteC(ctypes.Structure):
@@ -69,6 +72,21 @@ class _RequestsC(ctypes.Structure):
 class _BalanceC(ctypes.Structure):
     _fields_ = [("n_seq", ctypes.c_int32)] + [(n, ctypes.c_void_p) for n in (
         "seq_offsets", "valid", "counts", "mean_prob", "tokens", "totals", "loss")]
+
+
+class _NormC(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int32), ("eps", ctypes.c_float), ("weight", ctypes.c_void_p),
+                ("weight_dtype", ctypes.c_int32)]
+
+
+class _GradientC(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("grad_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+class _ClipItemC(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int32),
+                ("dtypes", ctypes.c_int32), ("order", ctypes.c_int64)]
 
 
 _lib = None
@@ -117,6 +135,25 @@ def _load():
         lib.coli_moe_balance_loss.argtypes = [P(_LayerC), vp, vp, i32, P(_BalanceC), vp, sz, vp]
         lib.coli_moe_route_backward.argtypes = [P(_LayerC), vp, vp, i32, vp, P(_BalanceC), vp, vp,
                                                 vp]
+        lib.coli_moe_norm_workspace_bytes.argtypes = [P(_NormC), i32]
+        lib.coli_moe_norm_workspace_bytes.restype = sz
+        lib.coli_moe_norm.argtypes = [P(_NormC), vp, vp, i32, i32, vp, vp, i32, vp, vp, vp]
+        lib.coli_moe_norm_backward.argtypes = [P(_NormC), vp, i32, vp, vp, i32, vp, vp, vp, vp, sz,
+                                               vp]
+        lib.coli_moe_forward_prefill_quantized.argtypes = [P(_LayerC), P(_RouteC), vp, vp, i32, vp,
+                                                           i32, vp, sz, vp]
+        lib.coli_moe_dispatch.argtypes = [P(_LayerC), P(_RouteC), vp, i32, i32, vp, i64, vp]
+        lib.coli_moe_dispatch_backward.argtypes = [P(_LayerC), P(_RouteC), vp, i32, i64, vp, i32,
+                                                   vp, i32, vp]
+        lib.coli_moe_combine.argtypes = lib.coli_moe_dispatch_backward.argtypes
+        lib.coli_moe_combine_backward.argtypes = [P(_LayerC), P(_RouteC), vp, i32, i64, vp, i32,
+                                                  i32, vp, vp, vp]
+        lib.coli_moe_clip_items.argtypes = [P(_GradientC), i32]
+        lib.coli_moe_clip_items.restype = i64
+        lib.coli_moe_clip_plan.argtypes = [P(_GradientC), i32, vp, i64]
+        lib.coli_moe_clip_workspace_bytes.argtypes = []
+        lib.coli_moe_clip_workspace_bytes.restype = sz
+        lib.coli_moe_clip_gradients.argtypes = [vp, i64, ctypes.c_float, vp, vp, sz, vp]
         lib.coli_moe_strerror.argtypes = [ctypes.c_int]
         lib.coli_moe_strerror.restype = ctypes.c_char_p
         lib.coli_moe_set_trace.argtypes = [ctypes.POINTER(_TraceC)]
@@ -129,7 +166,10 @@ def _load():
                   "coli_moe_quantize_mxfp4", "coli_moe_read_probe",
                   "coli_moe_mfma_probe", "coli_moe_quantize_mxfp8", "coli_moe_mx_dots",
                   "coli_moe_project", "coli_moe_project_backward", "coli_moe_balance_loss",
-                  "coli_moe_route_backward"):
+                  "coli_moe_route_backward", "coli_moe_norm", "coli_moe_norm_backward",
+                  "coli_moe_forward_prefill_quantized", "coli_moe_dispatch",
+                  "coli_moe_dispatch_backward", "coli_moe_combine", "coli_moe_combine_backward",
+                  "coli_moe_clip_plan", "coli_moe_clip_gradients"):
             getattr(lib, f).restype = ctypes.c_int
         _lib = lib
     return _lib
@@ -494,6 +534,195 @@ def coli_moe_route_backward(layer: Layer, logits, topk_idx, T: int, d_topk_w, ba
     _run("coli_moe_route_backward", logits, stream, ctypes.byref(layer.c), logits.data_ptr(),
          topk_idx.data_ptr(), T, _ptr(d_topk_w),
          None if balance is None else ctypes.byref(balance.c), _ptr(d_loss), d_logits.data_ptr())
+
+
+_DTYPES = {torch.bfloat16: COLI_SRC_BF16, torch.float32: COLI_SRC_F32}
+
+
+def _dtype(t, name):
+    """COLI_SRC_* of a tensor (bf16 where there is none)."""
+    if t is None:
+        return COLI_SRC_BF16
+    if t.dtype not in _DTYPES:
+        raise ValueError("%s: expected a bfloat16 or float32 tensor, got %s" % (name, t.dtype))
+    return _DTYPES[t.dtype]
+
+
+class Norm:
+    """A root-mean-square norm over `hidden` values: weight [hidden] bf16 or
+    fp32 on the device (None: ones)."""
+
+    def __init__(self, hidden: int, weight=None, eps: float = 1e-6):
+        if weight is not None:
+            _dtype(weight, "weight")
+            _need(weight, "weight", weight.dtype, hidden, weight.get_device())
+        self.weight, self.hidden = weight, hidden  # keep the tensor alive
+        self.c = _NormC(hidden, eps, _ptr(weight), _dtype(weight, "weight"))
+
+
+def coli_moe_norm_workspace_bytes(norm: Norm, T: int) -> int:
+    return int(_load().coli_moe_norm_workspace_bytes(ctypes.byref(norm.c), T))
+
+
+def norm_workspace(norm: Norm, T: int, device="cuda") -> torch.Tensor:
+    """A device buffer large enough for coli_moe_norm_backward at T rows."""
+    return torch.empty(max(coli_moe_norm_workspace_bytes(norm, T), 256), dtype=torch.uint8,
+                       device=device if norm.weight is None else norm.weight.device)
+
+
+def _norm_weight(norm, dev, x):
+    if norm.weight is not None and norm.weight.get_device() != dev:
+        raise ValueError("the norm's weight on %s, its input on %s"
+                         % (norm.weight.device, x.device))
+
+
+def coli_moe_norm(norm: Norm, x, residual, total, T: int, y, fmt: int = COLI_NORM_PLAIN, q=None,
+                  scales=None, stream=None):
+    """total = residual + x; y (bf16) and the codes q, scales of its norm (see
+    include/coli_moe.h).  residual and total, y, or q and scales may be None;
+    q int8 and scales fp16 for Q8_0, both uint8 for MXFP8."""
+    n, dev = T * norm.hidden, x.get_device()
+    _norm_weight(norm, dev, x)
+    _need(x, "x", torch.bfloat16, n, dev)
+    _need(y, "y", torch.bfloat16, n, dev)
+    rd = _dtype(residual, "residual")
+    if residual is not None:
+        _need(residual, "residual", residual.dtype, n, dev)
+        _need(total, "total", residual.dtype, n, dev)
+    if fmt == COLI_NORM_Q8_0:
+        _need(q, "q", torch.int8, n, dev)
+        _need(scales, "scales", torch.float16, n // 32, dev)
+    elif fmt == COLI_NORM_MXFP8:
+        _need(q, "q", torch.uint8, n, dev)
+        _need(scales, "scales", torch.uint8, n // 32, dev)
+    _run("coli_moe_norm", x, stream, ctypes.byref(norm.c), x.data_ptr(), _ptr(residual), rd, T,
+         _ptr(total), _ptr(y), fmt, _ptr(q), _ptr(scales))
+
+
+def coli_moe_norm_backward(norm: Norm, total, T: int, dy, d_total, dx, d_residual, d_weight,
+                           ws=None, stream=None):
+    """dx (bf16), d_residual (total's type) and d_weight (fp32) of coli_moe_norm
+    from total (x where there was no residual); d_total and any of the outputs
+    may be None, ws too without d_weight."""
+    n, dev = T * norm.hidden, total.get_device()
+    _norm_weight(norm, dev, total)
+    td = _dtype(total, "total")
+    _need(total, "total", total.dtype, n, dev)
+    _need(dy, "dy", torch.bfloat16, n, dev)
+    _need(d_total, "d_total", total.dtype, n, dev)
+    _need(dx, "dx", torch.bfloat16, n, dev)
+    _need(d_residual, "d_residual", total.dtype, n, dev)
+    _need(d_weight, "d_weight", torch.float32, norm.hidden, dev)
+    _run("coli_moe_norm_backward", total, stream, ctypes.byref(norm.c), total.data_ptr(), td,
+         dy.data_ptr(), _ptr(d_total), T, _ptr(dx), _ptr(d_residual), _ptr(d_weight),
+         *((None, 0) if ws is None else _ws(ws, total)))
+
+
+def coli_moe_forward_prefill_quantized(layer: Layer, route: Route, q, scales, T: int, y,
+                                       y_dtype: int, ws, stream=None):
+    """coli_moe_forward_prefill of the codes that coli_moe_norm writes."""
+    dev, mx = q.get_device(), bool(layer.c.flags & COLI_ACT_MXFP8)
+    _need(q, "q", torch.uint8 if mx else torch.int8, T * layer.hidden, dev)
+    _need(scales, "scales", torch.uint8 if mx else torch.float16, T * layer.hidden // 32, dev)
+    _need(y, "y", torch.float32 if y_dtype == COLI_OUT_F32 else torch.bfloat16, T * layer.hidden,
+          dev)
+    _need(route.topk_w, "route", torch.float32, T * layer.top_k, dev)
+    _run("coli_moe_forward_prefill_quantized", q, stream, ctypes.byref(layer.c),
+         ctypes.byref(route.c), q.data_ptr(), scales.data_ptr(), T, y.data_ptr(), y_dtype,
+         *_ws(ws, q))
+
+
+def _rows_args(layer, route, rows, beside, token, T):
+    """Device, types and rows of the calls on rows by expert: `rows` is a buffer
+    of rows, `token` and `beside` are by token."""
+    dev, h = rows.get_device(), layer.hidden
+    rd, td = _dtype(rows, "rows"), _dtype(token, "y")
+    _need(rows, "rows", rows.dtype, h, dev)
+    _need(token, "y", token.dtype, T * h, dev)
+    _need(beside, "beside", rows.dtype, T * h, dev)
+    _need(route.pair_pos, "route", torch.int32, T * layer.top_k, dev)
+    return rd, td, rows.numel() // h
+
+
+def coli_moe_dispatch(layer: Layer, route: Route, x, T: int, rows, stream=None):
+    """rows[pair_pos[t*k + j]] = x[t]; x and rows both bf16 or both fp32."""
+    rd, td, n = _rows_args(layer, route, rows, None, x, T)
+    if rd != td:
+        raise ValueError("x of %s, rows of %s" % (x.dtype, rows.dtype))
+    _run("coli_moe_dispatch", x, stream, ctypes.byref(layer.c), ctypes.byref(route.c),
+         x.data_ptr(), rd, T, rows.data_ptr(), n)
+
+
+def coli_moe_dispatch_backward(layer: Layer, route: Route, d_rows, beside, T: int, dx,
+                               stream=None):
+    """dx[t] = sum over t's pairs of d_rows (+ beside, of d_rows' type, or None)."""
+    rd, td, n = _rows_args(layer, route, d_rows, beside, dx, T)
+    _run("coli_moe_dispatch_backward", dx, stream, ctypes.byref(layer.c), ctypes.byref(route.c),
+         d_rows.data_ptr(), rd, n, _ptr(beside), T, dx.data_ptr(), td)
+
+
+def coli_moe_combine(layer: Layer, route: Route, rows, beside, T: int, y, stream=None):
+    """y[t] = sum over t's pairs of topk_w * rows (+ beside, of rows' type, or None)."""
+    rd, td, n = _rows_args(layer, route, rows, beside, y, T)
+    _run("coli_moe_combine", y, stream, ctypes.byref(layer.c), ctypes.byref(route.c),
+         rows.data_ptr(), rd, n, _ptr(beside), T, y.data_ptr(), td)
+
+
+def coli_moe_combine_backward(layer: Layer, route: Route, rows, dy, T: int, d_rows, d_topk_w,
+                              stream=None):
+    """d_rows (of rows' type) and d_topk_w (fp32) of coli_moe_combine; either may
+    be None, and rows too without d_topk_w."""
+    rd, td, n = _rows_args(layer, route, d_rows if rows is None else rows, None, dy, T)
+    if rows is not None and d_rows is not None:
+        _need(d_rows, "d_rows", rows.dtype, n * layer.hidden, rows.get_device())
+    _need(d_topk_w, "d_topk_w", torch.float32, T * layer.top_k, dy.get_device())
+    _run("coli_moe_combine_backward", dy, stream, ctypes.byref(layer.c), ctypes.byref(route.c),
+         _ptr(rows), rd, n, dy.data_ptr(), td, T, _ptr(d_rows), _ptr(d_topk_w))
+
+
+class Gradients:
+    """A plan for clipping `grads` (bf16 or fp32 tensors on one device), in place
+    or into `out` (as many tensors of the same sizes, of either type)."""
+
+    def __init__(self, grads, out=None):
+        self.grads = list(grads)
+        self.out = self.grads if out is None else list(out)
+        if not self.grads or len(self.out) != len(self.grads):
+            raise ValueError("%d gradients and %d outputs" % (len(self.grads), len(self.out)))
+        dev = self.grads[0].get_device()
+        c = (_GradientC * len(self.grads))()
+        for i, (g, o) in enumerate(zip(self.grads, self.out)):
+            kinds = _dtype(g, "grads[%d]" % i), _dtype(o, "out[%d]" % i)
+            _need(g, "grads[%d]" % i, g.dtype, 0, dev)
+            _need(o, "out[%d]" % i, o.dtype, 0, dev)
+            if g.numel() != o.numel():
+                raise ValueError("grads[%d] of %d elements, its output of %d"
+                                 % (i, g.numel(), o.numel()))
+            c[i] = _GradientC(_ptr(g), _ptr(o), g.numel(), *kinds)
+        lib = _load()
+        self.n = lib.coli_moe_clip_items(c, len(c))
+        if self.n < 0:
+            raise ColiError("coli_moe_clip_items", self.n)
+        plan = torch.empty(max(self.n, 1) * ctypes.sizeof(_ClipItemC), dtype=torch.uint8)
+        _check("coli_moe_clip_plan", lib.coli_moe_clip_plan(c, len(c), plan.data_ptr(), self.n))
+        self.items = plan.to(self.grads[0].device)
+
+
+def coli_moe_clip_workspace_bytes() -> int:
+    return int(_load().coli_moe_clip_workspace_bytes())
+
+
+def clip_workspace(device="cuda") -> torch.Tensor:
+    """A device buffer large enough for coli_moe_clip_gradients."""
+    return torch.empty(coli_moe_clip_workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+def coli_moe_clip_gradients(gradients: Gradients, max_norm: float, norm, ws, stream=None):
+    """norm [2] fp32 = the norm over all gradients, and the factor that they are
+    multiplied by: max_norm / norm above max_norm, else 1."""
+    _need(norm, "norm", torch.float32, 2, gradients.items.get_device())
+    _run("coli_moe_clip_gradients", gradients.items, stream, gradients.items.data_ptr(),
+         gradients.n, max_norm, norm.data_ptr(), *_ws(ws, gradients.items))
 
 
 def _hip_runtime():

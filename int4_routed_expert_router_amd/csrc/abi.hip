@@ -144,6 +144,31 @@ int check_balance(const Layer &L, const coli_moe_balance_t *b, bool outputs) {
   return COLI_OK;
 }
 
+bool is_dtype(int d) { return d == COLI_SRC_BF16 || d == COLI_SRC_F32; }
+
+constexpr int kMaxNormRows = 1 << 24;
+constexpr int64_t kMaxRows = int64_t(1) << 21;  // rows by expert
+
+int check_norm(const coli_moe_norm_t *n, int T) {
+  if (!n || n->hidden < 8 || n->hidden > kMaxHidden || n->hidden % 8) return COLI_E_INVALID;
+  if (!isfinite(n->eps) || !(n->eps > 0.0f)) return COLI_E_INVALID;
+  if (n->weight && !is_dtype(n->weight_dtype)) return COLI_E_INVALID;
+  if (T < 1 || T > kMaxNormRows) return COLI_E_INVALID;
+  return aligned(n->weight, 16) ? COLI_OK : COLI_E_ALIGN;
+}
+
+// What the calls on rows by expert have in common.
+int check_rows(const coli_moe_layer_t *layer, const coli_moe_route_t *r, int T, int64_t n_rows,
+               int dtype, int other_dtype, bool weights, Layer *L) {
+  int rc = check_layer(layer, L);
+  if (rc) return rc;
+  if (!r || !r->pair_pos || (weights && !r->topk_w)) return COLI_E_INVALID;
+  if ((rc = check_tokens(*L, T, kMaxT))) return rc;
+  if (n_rows < 1 || n_rows > kMaxRows || !is_dtype(dtype) || !is_dtype(other_dtype))
+    return COLI_E_INVALID;
+  return aligned(r->pair_pos, 4) && aligned(r->topk_w, 4) ? COLI_OK : COLI_E_ALIGN;
+}
+
 }  // namespace
 }  // namespace coli
 
@@ -273,7 +298,22 @@ int coli_moe_forward_prefill(const coli_moe_layer_t *layer, const coli_moe_route
   Layer L;
   const int rc = check_forward(layer, route, x, T, y, y_dtype, ws, ws_bytes, COLI_ENTRY_PREFILL, &L);
   if (rc) return rc;
-  return launch_prefill(L, *route, x, T, y, y_dtype, ws, reinterpret_cast<hipStream_t>(stream));
+  return launch_prefill(L, *route, x, nullptr, nullptr, T, y, y_dtype, ws,
+                        reinterpret_cast<hipStream_t>(stream));
+}
+
+int coli_moe_forward_prefill_quantized(const coli_moe_layer_t *layer,
+                                       const coli_moe_route_t *route, const void *q,
+                                       const void *scales, int32_t T, void *y, int32_t y_dtype,
+                                       void *ws, size_t ws_bytes, void *stream) {
+  Layer L;
+  const int rc = check_forward(layer, route, reinterpret_cast<const uint16_t *>(q), T, y, y_dtype,
+                               ws, ws_bytes, COLI_ENTRY_PREFILL, &L);
+  if (rc) return rc;
+  if (!scales) return COLI_E_INVALID;
+  if (!aligned(scales, 16)) return COLI_E_ALIGN;
+  return launch_prefill(L, *route, nullptr, q, scales, T, y, y_dtype, ws,
+                        reinterpret_cast<hipStream_t>(stream));
 }
 
 int coli_moe_quantize_q8_0(const void *src, int32_t src_dtype, int64_t n, int8_t *q,
@@ -454,6 +494,115 @@ int coli_moe_route_backward(const coli_moe_layer_t *layer, const float *logits,
                                reinterpret_cast<hipStream_t>(stream));
 }
 
+size_t coli_moe_norm_workspace_bytes(const coli_moe_norm_t *norm, int32_t T) {
+  return check_norm(norm, T) ? 0 : norm_workspace(norm->hidden, T);
+}
+
+int coli_moe_norm(const coli_moe_norm_t *norm, const uint16_t *x, const void *residual,
+                  int32_t residual_dtype, int32_t T, void *total, uint16_t *y, int32_t format,
+                  void *q, void *scales, void *stream) {
+  const int rc = check_norm(norm, T);
+  if (rc) return rc;
+  if (!x || !residual != !total || (residual && !is_dtype(residual_dtype))) return COLI_E_INVALID;
+  if (format != COLI_NORM_PLAIN && format != COLI_NORM_Q8_0 && format != COLI_NORM_MXFP8)
+    return COLI_E_INVALID;
+  const bool codes = format != COLI_NORM_PLAIN;
+  if (!q != !codes || !scales != !codes || (!y && !q)) return COLI_E_INVALID;
+  if (codes && norm->hidden % 32) return COLI_E_UNSUPPORTED;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(total, 16) || !aligned(y, 16) ||
+      !aligned(q, 16) || !aligned(scales, 4))
+    return COLI_E_ALIGN;
+  return launch_norm(*norm, x, residual, residual_dtype, T, total, y, format, q, scales,
+                     reinterpret_cast<hipStream_t>(stream));
+}
+
+int coli_moe_norm_backward(const coli_moe_norm_t *norm, const void *total, int32_t total_dtype,
+                           const uint16_t *dy, const void *d_total, int32_t T, uint16_t *dx,
+                           void *d_residual, float *d_weight, void *ws, size_t ws_bytes,
+                           void *stream) {
+  int rc = check_norm(norm, T);
+  if (rc) return rc;
+  if (!total || !is_dtype(total_dtype) || !dy || (!dx && !d_residual && !d_weight))
+    return COLI_E_INVALID;
+  if (!aligned(total, 16) || !aligned(dy, 16) || !aligned(d_total, 16) || !aligned(dx, 16) ||
+      !aligned(d_residual, 16) || !aligned(d_weight, 16))
+    return COLI_E_ALIGN;
+  if (d_weight && (rc = check_ws(ws, ws_bytes, norm_workspace(norm->hidden, T)))) return rc;
+  return launch_norm_backward(*norm, total, total_dtype, dy, d_total, T, dx, d_residual, d_weight,
+                              ws, reinterpret_cast<hipStream_t>(stream));
+}
+
+int coli_moe_dispatch(const coli_moe_layer_t *layer, const coli_moe_route_t *route, const void *x,
+                      int32_t dtype, int32_t T, void *rows, int64_t n_rows, void *stream) {
+  Layer L;
+  const int rc = check_rows(layer, route, T, n_rows, dtype, dtype, false, &L);
+  if (rc) return rc;
+  if (!x || !rows) return COLI_E_INVALID;
+  if (!aligned(x, 16) || !aligned(rows, 16)) return COLI_E_ALIGN;
+  return launch_dispatch(L, route->pair_pos, x, dtype, T, rows, n_rows,
+                         reinterpret_cast<hipStream_t>(stream));
+}
+
+int coli_moe_dispatch_backward(const coli_moe_layer_t *layer, const coli_moe_route_t *route,
+                               const void *d_rows, int32_t rows_dtype, int64_t n_rows,
+                               const void *beside, int32_t T, void *dx, int32_t dx_dtype,
+                               void *stream) {
+  Layer L;
+  const int rc = check_rows(layer, route, T, n_rows, rows_dtype, dx_dtype, false, &L);
+  if (rc) return rc;
+  if (!d_rows || !dx) return COLI_E_INVALID;
+  if (!aligned(d_rows, 16) || !aligned(beside, 16) || !aligned(dx, 16)) return COLI_E_ALIGN;
+  return launch_rows_combine(L, route->pair_pos, nullptr, d_rows, rows_dtype, n_rows, beside, T,
+                             dx, dx_dtype, reinterpret_cast<hipStream_t>(stream));
+}
+
+int coli_moe_combine(const coli_moe_layer_t *layer, const coli_moe_route_t *route,
+                     const void *rows, int32_t rows_dtype, int64_t n_rows, const void *beside,
+                     int32_t T, void *y, int32_t y_dtype, void *stream) {
+  Layer L;
+  const int rc = check_rows(layer, route, T, n_rows, rows_dtype, y_dtype, true, &L);
+  if (rc) return rc;
+  if (!rows || !y) return COLI_E_INVALID;
+  if (!aligned(rows, 16) || !aligned(beside, 16) || !aligned(y, 16)) return COLI_E_ALIGN;
+  return launch_rows_combine(L, route->pair_pos, route->topk_w, rows, rows_dtype, n_rows, beside,
+                             T, y, y_dtype, reinterpret_cast<hipStream_t>(stream));
+}
+
+int coli_moe_combine_backward(const coli_moe_layer_t *layer, const coli_moe_route_t *route,
+                              const void *rows, int32_t rows_dtype, int64_t n_rows,
+                              const void *dy, int32_t dy_dtype, int32_t T, void *d_rows,
+                              float *d_topk_w, void *stream) {
+  Layer L;
+  const int rc = check_rows(layer, route, T, n_rows, rows_dtype, dy_dtype, true, &L);
+  if (rc) return rc;
+  if (!dy || (!d_rows && !d_topk_w) || (d_topk_w && !rows)) return COLI_E_INVALID;
+  if (!aligned(rows, 16) || !aligned(dy, 16) || !aligned(d_rows, 16) || !aligned(d_topk_w, 4))
+    return COLI_E_ALIGN;
+  return launch_combine_backward(L, route->pair_pos, route->topk_w, rows, rows_dtype, n_rows, dy,
+                                 dy_dtype, T, d_rows, d_topk_w,
+                                 reinterpret_cast<hipStream_t>(stream));
+}
+
+int64_t coli_moe_clip_items(const coli_moe_gradient_t *gradients, int32_t n) {
+  return clip_items(gradients, n);
+}
+
+int coli_moe_clip_plan(const coli_moe_gradient_t *gradients, int32_t n,
+                       coli_moe_clip_item_t *items, int64_t n_items) {
+  return clip_plan(gradients, n, items, n_items);
+}
+
+size_t coli_moe_clip_workspace_bytes(void) { return clip_workspace(); }
+
+int coli_moe_clip_gradients(const coli_moe_clip_item_t *items, int64_t n_items, float max_norm,
+                            float *norm, void *ws, size_t ws_bytes, void *stream) {
+  if (n_items < 0 || (n_items && !items) || !norm || !(max_norm >= 0.0f)) return COLI_E_INVALID;
+  if (!aligned(items, 8) || !aligned(norm, 4)) return COLI_E_ALIGN;
+  const int rc = check_ws(ws, ws_bytes, clip_workspace());
+  if (rc) return rc;
+  return launch_clip(items, n_items, max_norm, norm, ws, reinterpret_cast<hipStream_t>(stream));
+}
+
 int coli_moe_set_trace(coli_moe_trace_t *trace) {
   if (trace && (!trace->start || !trace->stop || !trace->kernel || trace->capacity < 0))
     return COLI_E_INVALID;
@@ -473,6 +622,6 @@ const char *coli_moe_strerror(int status) {
   }
 }
 
-const char *coli_moe_version(void) { return "0.2.0"; }
+const char *coli_moe_version(void) { return "0.3.0"; }
 
 }  // extern "C"

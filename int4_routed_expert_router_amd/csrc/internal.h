@@ -43,8 +43,9 @@ int launch_route(const Layer &L, const float *logits, const float *sel_bias, int
                  const coli_moe_route_t &r, hipStream_t s);
 int launch_decode(const Layer &L, const coli_moe_route_t &r, const uint16_t *x, int T,
                   void *y, int y_dtype, void *ws, hipStream_t s);
-int launch_prefill(const Layer &L, const coli_moe_route_t &r, const uint16_t *x, int T,
-                   void *y, int y_dtype, void *ws, hipStream_t s);
+// x in bf16, or quantised already (codes and scales; x is then NULL)
+int launch_prefill(const Layer &L, const coli_moe_route_t &r, const uint16_t *x, const void *q,
+                   const void *scales, int T, void *y, int y_dtype, void *ws, hipStream_t s);
 // Router logits x . W_r^T (router.hip).
 int launch_router_logits(const Layer &L, const uint16_t *w, const uint16_t *x, int T,
                          float *logits, hipStream_t s);
@@ -90,6 +91,31 @@ int launch_balance(const Layer &L, const float *logits, const int32_t *idx, int 
 int launch_route_backward(const Layer &L, const float *logits, const int32_t *idx, int T,
                           const float *d_w, const coli_moe_balance_t *b, const float *d_loss,
                           float *d_logits, hipStream_t s);
+
+// The norm in front of the layer (norm.hip).
+size_t norm_workspace(int H, int T);
+int launch_norm(const coli_moe_norm_t &n, const uint16_t *x, const void *residual,
+                int residual_dtype, int T, void *total, uint16_t *y, int format, void *q,
+                void *scales, hipStream_t s);
+int launch_norm_backward(const coli_moe_norm_t &n, const void *total, int total_dtype,
+                         const uint16_t *dy, const void *d_total, int T, uint16_t *dx,
+                         void *d_residual, float *d_weight, void *ws, hipStream_t s);
+// Rows sorted by expert and back (rows.hip); w NULL: all ones.
+int launch_dispatch(const Layer &L, const int32_t *pos, const void *x, int dtype, int T,
+                    void *rows, int64_t n_rows, hipStream_t s);
+int launch_rows_combine(const Layer &L, const int32_t *pos, const float *w, const void *rows,
+                        int rows_dtype, int64_t n_rows, const void *beside, int T, void *y,
+                        int y_dtype, hipStream_t s);
+int launch_combine_backward(const Layer &L, const int32_t *pos, const float *w, const void *rows,
+                            int rows_dtype, int64_t n_rows, const void *dy, int dy_dtype, int T,
+                            void *d_rows, float *d_w, hipStream_t s);
+// Clipping by the global norm (clip.hip); plans are made on the host.
+int64_t clip_items(const coli_moe_gradient_t *g, int32_t n);
+int clip_plan(const coli_moe_gradient_t *g, int32_t n, coli_moe_clip_item_t *items,
+              int64_t n_items);
+size_t clip_workspace();
+int launch_clip(const coli_moe_clip_item_t *items, int64_t n_items, float max_norm, float *norm,
+                void *ws, hipStream_t s);
 
 inline int hip_status(hipError_t e) { return e == hipSuccess ? COLI_OK : COLI_E_HIP; }
 

@@ -21,6 +21,7 @@
 //             channels (one wavefront holds exactly one block per token).
 //             down epilogue: fp32 o rows.
 //  combine  : shared with decode (fixed-order weighted sum).
+#include "act_codec.h"
 #include "device_common.h"
 #include "internal.h"
 
@@ -119,6 +120,25 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const void *__restri
     rec[b] = make_float2(-kMagicF * df, df);
   } else {
     d[b] = d16;
+  }
+}
+
+// What quantize_kernel<true> writes, from Q8_0 codes and scales that are there
+// already: half a block to a thread, n halves.
+__global__ void __launch_bounds__(kThreads) reorder_kernel(const uint4 *__restrict__ q,
+                                                           const uint16_t *__restrict__ d,
+                                                           int64_t n, uint4 *__restrict__ out,
+                                                           float2 *__restrict__ rec) {
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= n) return;
+  const uint4 u = q[i];
+  out[i] = make_uint4(__builtin_amdgcn_perm(u.y, u.x, 0x06040200u),
+                      __builtin_amdgcn_perm(u.y, u.x, 0x07050301u),
+                      __builtin_amdgcn_perm(u.w, u.z, 0x06040200u),
+                      __builtin_amdgcn_perm(u.w, u.z, 0x07050301u));
+  if ((i & 1) == 0) {
+    const float df = f16_to_f32(d[i >> 1]);
+    rec[i >> 1] = make_float2(-kMagicF * df, df);
   }
 }
 
@@ -1393,16 +1413,6 @@ dgemm_kernel(GemmArgs g, coli_moe_route_t r, const int4 *__restrict__ tiles,
 typedef int coli_i32x8 __attribute__((ext_vector_type(8)));
 typedef float coli_f32x4v __attribute__((ext_vector_type(4)));
 
-// E8M0 shared exponent of a 32-block with maximum magnitude amax:
-// floor(log2 amax) - 8 (the largest E4M3 exponent) + 127, clamped to
-// [0, 254]; 0 for an all-zero block.  floor(log2) comes from the fp32
-// exponent field; a subnormal amax clamps to 0 anyway.
-COLI_DEV uint32_t mx8_exponent(float amax) {
-  const int ex = (int)((__float_as_uint(amax) >> 23) & 0xffu);  // biased; 0 for 0 / subnormal
-  const int E = ex - 127 - 8 + 127;
-  return amax > 0.0f ? (uint32_t)max(0, min(254, E)) : 0u;
-}
-
 // E4M3 code of v / 2^(E-127) (v fp32), nearest with ties to the even code,
 // saturating at 448, sign kept (also for zero).  The scaled magnitude m is
 // exact (a power-of-two scaling; only values far below the smallest code
@@ -1785,10 +1795,16 @@ int launch_mx_dots(const Layer &L, int expert, int matrix, const uint8_t *qa, co
 namespace {
 
 // The int4 forward on the DMA GEMM (dgemm_layer).
-int launch_prefill_dgemm(const Layer &L, const coli_moe_route_t &r, const uint16_t *x, int T,
-                         void *y, int y_dtype, const PrefillWs &w, hipStream_t s) {
-  {
-    const int64_t nb = (int64_t)T * L.H / 32;
+int launch_prefill_dgemm(const Layer &L, const coli_moe_route_t &r, const uint16_t *x,
+                         const void *q, const void *scales, int T, void *y, int y_dtype,
+                         const PrefillWs &w, hipStream_t s) {
+  const int64_t nb = (int64_t)T * L.H / 32;
+  if (q) {
+    launch_k(COLI_K_QUANTIZE, reorder_kernel, dim3((unsigned)((2 * nb + kThreads - 1) / kThreads)),
+             dim3(kThreads), 0, s, reinterpret_cast<const uint4 *>(q),
+             reinterpret_cast<const uint16_t *>(scales), 2 * nb, reinterpret_cast<uint4 *>(w.qx),
+             w.rx);
+  } else {
     launch_k(COLI_K_QUANTIZE, quantize_kernel<true>, dim3((unsigned)((nb + kThreads - 1) / kThreads)),
              dim3(kThreads), 0, s, (const void *)x, (int)COLI_SRC_BF16, nb, w.qx,
              (uint16_t *)nullptr, w.rx);
@@ -1839,12 +1855,17 @@ namespace {
 
 // The MX forward (MXFP4 weights, COLI_ACT_MXFP8): MXFP8 of x, plan, the two
 // MX GEMMs (h in MXFP8 between them), combine.
-int launch_prefill_mx(const Layer &L, const coli_moe_route_t &r, const uint16_t *x, int T,
-                      void *y, int y_dtype, const PrefillWs &w, hipStream_t s) {
-  uint8_t *qx = reinterpret_cast<uint8_t *>(w.qx), *ex = reinterpret_cast<uint8_t *>(w.dx);
+int launch_prefill_mx(const Layer &L, const coli_moe_route_t &r, const uint16_t *x, const void *q,
+                      const void *scales, int T, void *y, int y_dtype, const PrefillWs &w,
+                      hipStream_t s) {
   uint8_t *qh = reinterpret_cast<uint8_t *>(w.qh), *eh = reinterpret_cast<uint8_t *>(w.dh);
-  int rc = launch_quantize_mxfp8(x, COLI_SRC_BF16, (int64_t)T * L.H, qx, ex, s);
-  if (rc) return rc;
+  if (!q) {
+    uint8_t *qx = reinterpret_cast<uint8_t *>(w.qx), *ex = reinterpret_cast<uint8_t *>(w.dx);
+    const int rc = launch_quantize_mxfp8(x, COLI_SRC_BF16, (int64_t)T * L.H, qx, ex, s);
+    if (rc) return rc;
+    q = qx;
+    scales = ex;
+  }
   launch_k(COLI_K_PLAN, plan_kernel, dim3(1), dim3(1024), 0, s, r, T, L.k, L.E, L.S, w.tiles,
            w.ntiles);
   if (hipGetLastError() != hipSuccess) return COLI_E_HIP;
@@ -1856,8 +1877,8 @@ int launch_prefill_mx(const Layer &L, const coli_moe_route_t &r, const uint16_t 
     g.ws = L.scales;
     g.rows = L.I;
     g.K = L.H;
-    g.act = reinterpret_cast<const int8_t *>(qx);
-    g.act_d = reinterpret_cast<const uint16_t *>(ex);
+    g.act = reinterpret_cast<const int8_t *>(q);
+    g.act_d = reinterpret_cast<const uint16_t *>(scales);
     g.up_offset_q = (int64_t)L.I * L.H / 2;
     g.up_offset_s = (int64_t)L.I * L.H / 64;
     const int nn = (L.I + 63) / 64;
@@ -1888,13 +1909,18 @@ int launch_prefill_mx(const Layer &L, const coli_moe_route_t &r, const uint16_t 
 
 }  // namespace
 
-int launch_prefill(const Layer &L, const coli_moe_route_t &r, const uint16_t *x, int T, void *y,
-                   int y_dtype, void *ws, hipStream_t s) {
+int launch_prefill(const Layer &L, const coli_moe_route_t &r, const uint16_t *x, const void *q,
+                   const void *scales, int T, void *y, int y_dtype, void *ws, hipStream_t s) {
   const PrefillWs w = carve(L, T, ws);
-  if (L.f4 && (L.flags & COLI_ACT_MXFP8)) return launch_prefill_mx(L, r, x, T, y, y_dtype, w, s);
-  if (dgemm_layer(L)) return launch_prefill_dgemm(L, r, x, T, y, y_dtype, w, s);
-  int rc = launch_quantize_q8_0(x, COLI_SRC_BF16, (int64_t)T * L.H, w.qx, w.dx, s);
-  if (rc) return rc;
+  if (L.f4 && (L.flags & COLI_ACT_MXFP8))
+    return launch_prefill_mx(L, r, x, q, scales, T, y, y_dtype, w, s);
+  if (dgemm_layer(L)) return launch_prefill_dgemm(L, r, x, q, scales, T, y, y_dtype, w, s);
+  if (!q) {
+    const int rc = launch_quantize_q8_0(x, COLI_SRC_BF16, (int64_t)T * L.H, w.qx, w.dx, s);
+    if (rc) return rc;
+    q = w.qx;
+    scales = w.dx;
+  }
   launch_k(COLI_K_PLAN, plan_kernel, dim3(1), dim3(1024), 0, s, r, T, L.k, L.E, L.S, w.tiles,
            w.ntiles);
   if (hipGetLastError() != hipSuccess) return COLI_E_HIP;
@@ -1907,8 +1933,8 @@ int launch_prefill(const Layer &L, const coli_moe_route_t &r, const uint16_t *x,
     g.K = L.H;
     g.rs = L.w8 ? 0 : 1;
     const int wf = L.f4 ? kFmtF4 : (L.w8 ? kFmtI8 : kFmtI4);
-    g.act = w.qx;
-    g.act_d = w.dx;
+    g.act = reinterpret_cast<const int8_t *>(q);
+    g.act_d = reinterpret_cast<const uint16_t *>(scales);
     g.up_offset_q = ((int64_t)L.I * L.H) >> g.rs;
     g.up_offset_s = (int64_t)L.I * L.H / 64;
     const int nn = (L.I + 63) / 64;

@@ -1,0 +1,49 @@
+// values8.h -- eight neighbouring values of a bf16 or fp32 array, the unit in
+// which the row kernels move data (16 or 32 bytes).
+#pragma once
+
+#include "device_common.h"
+
+namespace coli {
+
+COLI_DEV void unpack8(const uint4 u, float v[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+COLI_DEV uint4 pack8(const float v[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = f32_to_bf16_bits(v[2 * i]) | (f32_to_bf16_bits(v[2 * i + 1]) << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Values 8i .. 8i+7 of p.
+template <bool F32>
+COLI_DEV void load8(const void *p, int64_t i, float v[8]) {
+  if (F32) {
+    const float4 a = reinterpret_cast<const float4 *>(p)[2 * i];
+    const float4 b = reinterpret_cast<const float4 *>(p)[2 * i + 1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    unpack8(reinterpret_cast<const uint4 *>(p)[i], v);
+  }
+}
+
+template <bool F32>
+COLI_DEV void store8(void *p, int64_t i, const float v[8]) {
+  if (F32) {
+    reinterpret_cast<float4 *>(p)[2 * i] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4 *>(p)[2 * i + 1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    reinterpret_cast<uint4 *>(p)[i] = pack8(v);
+  }
+}
+
+}  // namespace coli
