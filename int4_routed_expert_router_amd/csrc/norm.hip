@@ -2,12 +2,14 @@
 // addition, the norm and the prefill path's codes in one pass; its gradients.
 #include "act_codec.h"
 #include "internal.h"
+#include "lanes.h"
 #include "values8.h"
 
 namespace coli {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int block_of(int lanes) { return lanes > kThreads ? lanes : kThreads; }
 
 COLI_DEV void weight8(const void *w, int f32, int i, float v[8]) {
   if (!w) {
@@ -17,27 +19,6 @@ COLI_DEV void weight8(const void *w, int f32, int i, float v[8]) {
     load8<true>(w, i, v);
   } else {
     load8<false>(w, i, v);
-  }
-}
-
-// Sums of N values over the W waves that share a row (W = 1: the wave itself).
-template <int W, int N>
-COLI_DEV void row_sums(float (&v)[N], float (*red)[W]) {
-#pragma unroll
-  for (int n = 0; n < N; ++n) v[n] = wave_sum(v[n]);
-  if (W == 1) return;
-  const int wave = threadIdx.x >> 6;
-  __syncthreads();  // the last row's sums have been read
-  if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) red[n][wave] = v[n];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    v[n] = 0.0f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) v[n] += red[n][w];
   }
 }
 
@@ -56,18 +37,22 @@ struct NormArgs {
   float eps, inv_h;
 };
 
-// RES: 0 no residual, 1 bf16, 2 fp32.  A row is held by 256 lanes, NC chunks
+// RES: 0 no residual, 1 bf16, 2 fp32.  A row is held by LPR lanes, NC chunks
 // of eight values each.
-template <int NC, int RES>
-__global__ void __launch_bounds__(kThreads) norm_kernel(NormArgs g) {
-  __shared__ float red[1][4];
-  for (int64_t row = blockIdx.x; row < g.T; row += gridDim.x) {
+template <int LPR, int NC, int RES>
+__global__ void __launch_bounds__(block_of(LPR)) norm_kernel(NormArgs g) {
+  constexpr int B = block_of(LPR), RPB = B / LPR;  // rows of a workgroup
+  __shared__ float red[2][1][LPR > 64 ? LPR / 64 : 1];
+  const int li = threadIdx.x % LPR;
+  int turn = 0;
+  for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR; row < g.T;
+       row += (int64_t)gridDim.x * RPB, turn ^= 1) {
     const int64_t base = row * g.chunks;
     float v[NC][8];
     float sum[1] = {0.0f};
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int i = threadIdx.x + c * kThreads;
+      const int i = li + c * LPR;
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[c][j] = 0.0f;
       if (i < g.chunks) {
@@ -89,11 +74,11 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(NormArgs g) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum[0] = fmaf(v[c][j], v[c][j], sum[0]);
     }
-    row_sums<4, 1>(sum, red);
+    row_sums<LPR, 1>(sum, red[turn]);
     const float r = rsqrtf(fmaf(sum[0], g.inv_h, g.eps));
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int i = threadIdx.x + c * kThreads;
+      const int i = li + c * LPR;
       if (i >= g.chunks) continue;  // with codes, whole quads of lanes
       float w[8];
       weight8(g.weight, g.weight_f32, i, w);
@@ -117,17 +102,27 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(NormArgs g) {
   }
 }
 
+template <int RES, int LPR, int NC>
+void run_norm(const NormArgs &g, hipStream_t s) {
+  constexpr int B = block_of(LPR), RPB = B / LPR;
+  const int64_t blocks = ((int64_t)g.T + RPB - 1) / RPB;
+  launch_k(COLI_K_NORM, norm_kernel<LPR, NC, RES>,
+           dim3((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20))), dim3(B), 0, s, g);
+}
+
 template <int RES>
 void pick_norm(const NormArgs &g, hipStream_t s) {
-  const int nc = (g.chunks + kThreads - 1) / kThreads;
-  const int grid = g.T < (1 << 16) ? g.T : (1 << 16);
-  launch_k(COLI_K_NORM,
-           nc == 1   ? norm_kernel<1, RES>
-           : nc == 2 ? norm_kernel<2, RES>
-           : nc == 3 ? norm_kernel<3, RES>
-           : nc == 4 ? norm_kernel<4, RES>
-                     : norm_kernel<8, RES>,
-           dim3(grid), dim3(kThreads), 0, s, g);
+  const int n = g.chunks;
+  if (n <= 8) return run_norm<RES, 8, 1>(g, s);
+  if (n <= 16) return run_norm<RES, 16, 1>(g, s);
+  if (n <= 32) return run_norm<RES, 32, 1>(g, s);
+  if (n <= 64) return run_norm<RES, 64, 1>(g, s);
+  if (n <= 128) return run_norm<RES, 64, 2>(g, s);
+  if (n <= 256) return run_norm<RES, 256, 1>(g, s);
+  if (n <= 512) return run_norm<RES, 256, 2>(g, s);
+  if (n <= 768) return run_norm<RES, 256, 3>(g, s);
+  if (n <= 1024) return run_norm<RES, 256, 4>(g, s);
+  run_norm<RES, 1024, 2>(g, s);
 }
 
 // ----------------------------------------------------------------- backward
@@ -145,81 +140,152 @@ struct NormBackArgs {
   float eps, inv_h;
 };
 
-// d = r (n - h mean(n h)) + d_total with h = s r: both row sums, of s^2 and of
-// n s, come from the one pass that loads the row.  A workgroup takes the rows
-// blockIdx, blockIdx + grid, ... and keeps its part of d_weight in registers.
+// One lane's share of a row, as loaded.
 template <int NC, bool F32>
-__global__ void __launch_bounds__(kThreads) norm_backward_kernel(NormBackArgs g) {
-  __shared__ float red[2][4];
+struct BackRow {
+  uint4 s[NC][F32 ? 2 : 1], o[NC][F32 ? 2 : 1], dy[NC];
+};
+
+template <int LPR, int NC, bool F32>
+COLI_DEV void load_row(const NormBackArgs &g, int64_t row, int li, BackRow<NC, F32> &r) {
+  constexpr int U = F32 ? 2 : 1;
+  const int64_t base = row * g.chunks;
+  const uint4 *s = reinterpret_cast<const uint4 *>(g.total) + base * U;
+  const uint4 *o = reinterpret_cast<const uint4 *>(g.d_total) + base * U;
+  const uint4 *dy = reinterpret_cast<const uint4 *>(g.dy) + base;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int i = li + c * LPR;
+    const bool in = row < g.T && i < g.chunks;
+    r.dy[c] = in ? dy[i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      r.s[c][u] = in ? s[U * i + u] : make_uint4(0, 0, 0, 0);
+      r.o[c][u] = in && g.d_total ? o[U * i + u] : make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
+template <bool F32>
+COLI_DEV void unpack(const uint4 (&u)[F32 ? 2 : 1], float v[8]) {
+  if (F32) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint4 w = u[F32 ? j : 0];
+      v[4 * j] = __uint_as_float(w.x);
+      v[4 * j + 1] = __uint_as_float(w.y);
+      v[4 * j + 2] = __uint_as_float(w.z);
+      v[4 * j + 3] = __uint_as_float(w.w);
+    }
+  } else {
+    unpack8(u[0], v);
+  }
+}
+
+// d = r (n - h mean(n h)) + d_total with h = s r: both row sums, of s^2 and of
+// n s, come from the one pass that loads the row.  A workgroup goes over rows
+// with the next one's loads in flight, and keeps its part of d_weight in
+// registers.
+template <int LPR, int NC, bool F32>
+__global__ void __launch_bounds__(block_of(LPR)) norm_backward_kernel(NormBackArgs g) {
+  constexpr int B = block_of(LPR), RPB = B / LPR;  // rows of a workgroup
+  __shared__ float red[2][2][LPR > 64 ? LPR / 64 : 1];
+  const int li = threadIdx.x % LPR, ri = threadIdx.x / LPR;
   float dw[NC][8];
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[c][j] = 0.0f;
-  for (int64_t row = blockIdx.x; row < g.T; row += gridDim.x) {
-    const int64_t base = row * g.chunks;
-    float v[NC][8], dy[NC][8];
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t row = (int64_t)blockIdx.x * RPB + ri;
+  BackRow<NC, F32> a;
+  load_row<LPR>(g, row, li, a);
+  int turn = 0;
+  for (; row < g.T; row += step, turn ^= 1) {
+    BackRow<NC, F32> next;
+    load_row<LPR>(g, row + step, li, next);
     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int i = threadIdx.x + c * kThreads;
+      const int i = li + c * LPR;
+      float v[8], dy[8], w[8];
+      unpack<F32>(a.s[c], v);
+      unpack8(a.dy[c], dy);
+      weight8(i < g.chunks ? g.weight : nullptr, g.weight_f32, i, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[c][j] = dy[c][j] = 0.0f;
-      if (i < g.chunks) {
-        float w[8];
-        load8<F32>(g.total, base + i, v[c]);
-        load8<false>(g.dy, base + i, dy[c]);
-        weight8(g.weight, g.weight_f32, i, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          sum[0] = fmaf(v[c][j], v[c][j], sum[0]);
-          sum[1] = fmaf(dy[c][j] * w[j], v[c][j], sum[1]);
-        }
+      for (int j = 0; j < 8; ++j) {
+        sum[0] = fmaf(v[j], v[j], sum[0]);
+        sum[1] = fmaf(dy[j] * w[j], v[j], sum[1]);
       }
     }
-    row_sums<4, 2>(sum, red);
+    row_sums<LPR, 2>(sum, red[turn]);
     const float r = rsqrtf(fmaf(sum[0], g.inv_h, g.eps));
     const float m = sum[1] * g.inv_h * r;  // mean(n h)
+    const int64_t base = row * g.chunks;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int i = threadIdx.x + c * kThreads;
+      const int i = li + c * LPR;
       if (i >= g.chunks) continue;
-      float w[8], d[8];
+      float v[8], dy[8], o[8], w[8], d[8];
+      unpack<F32>(a.s[c], v);
+      unpack<F32>(a.o[c], o);
+      unpack8(a.dy[c], dy);
       weight8(g.weight, g.weight_f32, i, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float h = v[c][j] * r;
-        dw[c][j] = fmaf(dy[c][j], h, dw[c][j]);
-        d[j] = r * fmaf(-h, m, dy[c][j] * w[j]);
-      }
-      if (g.d_total) {
-        float o[8];
-        load8<F32>(g.d_total, base + i, o);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] += o[j];
+        const float h = v[j] * r;
+        dw[c][j] = fmaf(dy[j], h, dw[c][j]);
+        d[j] = fmaf(r, fmaf(-h, m, dy[j] * w[j]), o[j]);
       }
       if (g.dx) store8<false>(g.dx, base + i, d);
       if (g.d_residual) store8<F32>(g.d_residual, base + i, d);
     }
+    a = next;
   }
   if (!g.parts) return;
+  if (RPB == 1) {
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    const int i = threadIdx.x + c * kThreads;
-    if (i < g.chunks) store8<true>(g.parts, (int64_t)blockIdx.x * g.chunks + i, dw[c]);
+    for (int c = 0; c < NC; ++c) {
+      const int i = li + c * LPR;
+      if (i < g.chunks) store8<true>(g.parts, (int64_t)blockIdx.x * g.chunks + i, dw[c]);
+    }
+    return;
+  }
+  // the rows of a workgroup that went side by side
+  __shared__ float side[RPB > 1 ? RPB : 1][RPB > 1 ? LPR * NC * 8 : 1];
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) side[RPB > 1 ? ri : 0][RPB > 1 ? 8 * (li + c * LPR) + j : 0] = dw[c][j];
+  __syncthreads();
+  for (int c = threadIdx.x; c < 8 * g.chunks; c += B) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < RPB; ++k) sum += side[k][RPB > 1 ? c : 0];
+    g.parts[(int64_t)blockIdx.x * 8 * g.chunks + c] = sum;
   }
 }
 
 // Sums n parts of H columns in the order of the parts: 64 columns to a
-// workgroup, every 16th part to a wave.
+// workgroup, every 16th part to a wave, eight loads in flight.
 __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *__restrict__ parts, int n,
                                                            int H, float *__restrict__ out) {
   __shared__ float red[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = blockIdx.x * 64 + lane;
   float a = 0.0f;
-  if (c < H)
-    for (int p = wave; p < n; p += 16) a += parts[(int64_t)p * H + c];
+  if (c < H) {
+    for (int p0 = wave; p0 < n; p0 += 128) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int p = p0 + 16 * i;
+        v[i] = p < n ? parts[(int64_t)p * H + c] : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a += v[i];
+    }
+  }
   red[wave][lane] = a;
   __syncthreads();
   if (wave || c >= H) return;
@@ -229,25 +295,45 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *__restri
   out[c] = a;
 }
 
-// Workgroups of the backward pass, and parts of d_weight.
-int backward_groups(int T) { return T < 512 ? T : 512; }
+constexpr int kMaxParts = 512;
+
+// Lanes of a row in the backward pass, and its workgroups (the parts of
+// d_weight).
+int backward_lanes(int chunks) {
+  if (chunks <= 8) return 8;
+  if (chunks <= 16) return 16;
+  if (chunks <= 32) return 32;
+  if (chunks <= 128) return 64;
+  if (chunks <= 768) return 256;
+  return chunks <= 1024 ? 512 : 1024;
+}
+int backward_groups(int chunks, int T) {
+  const int lanes = backward_lanes(chunks), rows = block_of(lanes) / lanes;
+  const int groups = (T + rows - 1) / rows;
+  return groups < kMaxParts ? groups : kMaxParts;
+}
 
 template <bool F32>
 void pick_norm_backward(const NormBackArgs &g, hipStream_t s) {
-  const int nc = (g.chunks + kThreads - 1) / kThreads;
+  const int n = g.chunks, lanes = backward_lanes(n);
   launch_k(COLI_K_NORM_BACKWARD,
-           nc == 1   ? norm_backward_kernel<1, F32>
-           : nc == 2 ? norm_backward_kernel<2, F32>
-           : nc == 3 ? norm_backward_kernel<3, F32>
-           : nc == 4 ? norm_backward_kernel<4, F32>
-                     : norm_backward_kernel<8, F32>,
-           dim3(backward_groups(g.T)), dim3(kThreads), 0, s, g);
+           lanes == 8      ? norm_backward_kernel<8, 1, F32>
+           : lanes == 16   ? norm_backward_kernel<16, 1, F32>
+           : lanes == 32   ? norm_backward_kernel<32, 1, F32>
+           : lanes == 64   ? (n <= 64 ? norm_backward_kernel<64, 1, F32>
+                                      : norm_backward_kernel<64, 2, F32>)
+           : lanes == 256  ? (n <= 256   ? norm_backward_kernel<256, 1, F32>
+                              : n <= 512 ? norm_backward_kernel<256, 2, F32>
+                                         : norm_backward_kernel<256, 3, F32>)
+           : lanes == 512  ? norm_backward_kernel<512, 2, F32>
+                           : norm_backward_kernel<1024, 2, F32>,
+           dim3(backward_groups(n, g.T)), dim3(block_of(lanes)), 0, s, g);
 }
 
 }  // namespace
 
 size_t norm_workspace(int H, int T) {
-  return align_up((size_t)backward_groups(T) * H * sizeof(float));
+  return align_up((size_t)backward_groups(H / 8, T) * H * sizeof(float));
 }
 
 int launch_norm(const coli_moe_norm_t &n, const uint16_t *x, const void *residual,
@@ -299,7 +385,7 @@ int launch_norm_backward(const coli_moe_norm_t &n, const void *total, int total_
   if (hipGetLastError() != hipSuccess) return COLI_E_HIP;
   if (!d_weight) return COLI_OK;
   launch_k(COLI_K_NORM_REDUCE, norm_reduce_kernel, dim3((n.hidden + 63) / 64), dim3(1024), 0, s,
-           (const float *)ws, backward_groups(T), n.hidden, d_weight);
+           (const float *)ws, backward_groups(g.chunks, T), n.hidden, d_weight);
   return hip_status(hipGetLastError());
 }
 
