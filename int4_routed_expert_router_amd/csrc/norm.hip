@@ -266,36 +266,39 @@ __global__ void __launch_bounds__(block_of(LPR)) norm_backward_kernel(NormBackAr
   }
 }
 
-// Sums n parts of H columns in the order of the parts: 64 columns to a
-// workgroup, every 16th part to a wave, eight loads in flight.
+// Sums n parts of H columns: COLS columns to a workgroup, every (1024 / COLS)th
+// part to COLS lanes, sixteen loads in flight.  16 columns keep the chip busy
+// up to H = 2048 (1,024 parts of 2048: 4.2 us with an empty launch's 3.9; 64
+// columns: 5.7), 64 read whole lines of wider ones (512 parts of 6144: 4.1
+// against 5.3).
+template <int COLS>
 __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *__restrict__ parts, int n,
                                                            int H, float *__restrict__ out) {
-  __shared__ float red[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;
+  constexpr int G = 1024 / COLS;
+  __shared__ float red[G][COLS];
+  const int col = threadIdx.x % COLS, first = threadIdx.x / COLS;
+  const int c = blockIdx.x * COLS + col;
   float a = 0.0f;
   if (c < H) {
-    for (int p0 = wave; p0 < n; p0 += 128) {
-      float v[8];
+    for (int p0 = first; p0 < n; p0 += 16 * G) {
+      float v[16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int p = p0 + 16 * i;
+      for (int i = 0; i < 16; ++i) {
+        const int p = p0 + G * i;
         v[i] = p < n ? parts[(int64_t)p * H + c] : 0.0f;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a += v[i];
+      for (int i = 0; i < 16; ++i) a += v[i];
     }
   }
-  red[wave][lane] = a;
+  red[first][col] = a;
   __syncthreads();
-  if (wave || c >= H) return;
+  if (first != 0 || c >= H) return;
   a = 0.0f;
 #pragma unroll
-  for (int w = 0; w < 16; ++w) a += red[w][lane];
+  for (int j = 0; j < G; ++j) a += red[j][col];
   out[c] = a;
 }
-
-constexpr int kMaxParts = 512;
 
 // Lanes of a row in the backward pass, and its workgroups (the parts of
 // d_weight).
@@ -307,10 +310,14 @@ int backward_lanes(int chunks) {
   if (chunks <= 768) return 256;
   return chunks <= 1024 ? 512 : 1024;
 }
+// As many workgroups as the chip holds at once: their registers allow one of
+// 512 lanes and more to a CU, two of 256 lanes with two or three chunks, five
+// with one, of which four are used (more would only be more parts).
 int backward_groups(int chunks, int T) {
   const int lanes = backward_lanes(chunks), rows = block_of(lanes) / lanes;
+  const int most = lanes >= 512 ? 256 : chunks > 256 ? 512 : 1024;
   const int groups = (T + rows - 1) / rows;
-  return groups < kMaxParts ? groups : kMaxParts;
+  return groups < most ? groups : most;
 }
 
 template <bool F32>
@@ -384,8 +391,10 @@ int launch_norm_backward(const coli_moe_norm_t &n, const void *total, int total_
     pick_norm_backward<false>(g, s);
   if (hipGetLastError() != hipSuccess) return COLI_E_HIP;
   if (!d_weight) return COLI_OK;
-  launch_k(COLI_K_NORM_REDUCE, norm_reduce_kernel, dim3((n.hidden + 63) / 64), dim3(1024), 0, s,
-           (const float *)ws, backward_groups(g.chunks, T), n.hidden, d_weight);
+  const int H = n.hidden;
+  launch_k(COLI_K_NORM_REDUCE, H <= 2048 ? norm_reduce_kernel<16> : norm_reduce_kernel<64>,
+           dim3(H <= 2048 ? (H + 15) / 16 : (H + 63) / 64), dim3(1024), 0, s, (const float *)ws,
+           backward_groups(g.chunks, T), H, d_weight);
   return hip_status(hipGetLastError());
 }
 
