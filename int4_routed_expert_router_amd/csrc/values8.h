@@ -6,6 +6,25 @@
 
 namespace coli {
 
+// Loads and stores that leave the caches to others (NT), for buffers that are
+// several times the 256 MB of the chip's last cache: their own next reader
+// finds nothing of them there anyway.
+typedef unsigned int coli_u32x4 __attribute__((ext_vector_type(4)));
+template <bool NT>
+COLI_DEV uint4 load16(const uint4 *p) {
+  if (!NT) return *p;
+  const coli_u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const coli_u32x4 *>(p));
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
+template <bool NT>
+COLI_DEV void store16(uint4 *p, uint4 a) {
+  const coli_u32x4 v = {a.x, a.y, a.z, a.w};
+  if (NT)
+    __builtin_nontemporal_store(v, reinterpret_cast<coli_u32x4 *>(p));
+  else
+    *p = a;
+}
+
 COLI_DEV void unpack8(const uint4 u, float v[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
