@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(block_of(LPR)) combine_backward_kernel(RowArgs
       values8<DF32>(dy[c], f);
 #pragma unroll
       for (int j = 0; j < JB; ++j) {
+        if (j0 + j >= last) break;
         float e[8];
         values8<F32>(v[j][c], e);
         float d = 0.0f;
@@ -207,8 +208,8 @@ __global__ void __launch_bounds__(block_of(LPR)) combine_backward_kernel(RowArgs
     if (!g.d_w) continue;
 #pragma unroll
     for (int j = 0; j < JB; ++j) {
+      if (j0 + j >= last) break;
       const float s = lanes_sum<(LPR < 64 ? LPR : 64)>(dot[j]);
-      if (j0 + j >= last) continue;
       if (LPR <= 64) {
         if (li == 0) g.d_w[pair + j0 + j] = s;
       } else if ((threadIdx.x & 63) == 0) {
