@@ -118,8 +118,7 @@ COLI_DEV void item_scale(const void *g, void *o, int n, float f, int tid) {
             make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
     } else if (F32) {
       reinterpret_cast<uint2 *>(oat)[i] =
-          make_uint2(f32_to_bf16_bits(v[0]) | (f32_to_bf16_bits(v[1]) << 16),
-                     f32_to_bf16_bits(v[2]) | (f32_to_bf16_bits(v[3]) << 16));
+          make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
     } else {
       float w[8];
 #pragma unroll

@@ -9,7 +9,7 @@ namespace coli {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int block_of(int lanes) { return lanes > kThreads ? lanes : kThreads; }
+constexpr int block_of(int lanes) { return lanes > 64 ? lanes : kThreads; }
 
 COLI_DEV void weight8(const void *w, int f32, int i, float v[8]) {
   if (!w) {
@@ -310,23 +310,28 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *__restri
   out[c] = a;
 }
 
-// Lanes of a row in the backward pass, and its workgroups (the parts of
-// d_weight).
+// Lanes of a row in the backward pass: one chunk each up to 8192 values, as what
+// a lane keeps of a chunk (the row, the next one, d_weight) is 80 to 90
+// registers (8,192 x 6144: 256 lanes with three chunks 90 us, 768 with one 87;
+// 65,536 x 1024: 64 lanes with two 127, 128 with one 113).
 int backward_lanes(int chunks) {
   if (chunks <= 8) return 8;
   if (chunks <= 16) return 16;
   if (chunks <= 32) return 32;
-  if (chunks <= 128) return 64;
-  if (chunks <= 768) return 256;
-  return chunks <= 1024 ? 512 : 1024;
+  if (chunks <= 64) return 64;
+  if (chunks <= 128) return 128;
+  if (chunks <= 256) return 256;
+  if (chunks <= 512) return 512;
+  return chunks <= 768 ? 768 : 1024;
 }
-// As many workgroups as the chip holds at once: their registers allow one of
-// 512 lanes and more to a CU, two of 256 lanes with two or three chunks, five
-// with one, of which four are used (more would only be more parts).
+// Workgroups, and parts of d_weight: some 768 lanes to each of the 256 CUs.
+// More would be more parts and fewer rows to each (65,536 x 2048: 768
+// workgroups 219 us, 1,024 and 1,280 226; x 1024: 1,024 141, 1,536 and 2,048
+// 113; 8,192 x 6144: 256 87, 512 89).
 int backward_groups(int chunks, int T) {
-  const int lanes = backward_lanes(chunks), rows = block_of(lanes) / lanes;
-  const int most = lanes >= 512 ? 256 : chunks > 256 ? 512 : 1024;
-  const int groups = (T + rows - 1) / rows;
+  const int lanes = backward_lanes(chunks), block = block_of(lanes);
+  const int groups = (T + block / lanes - 1) / (block / lanes);
+  const int most = 256 * ((768 + block - 1) / block);
   return groups < most ? groups : most;
 }
 
@@ -337,12 +342,12 @@ void pick_norm_backward(const NormBackArgs &g, hipStream_t s) {
            lanes == 8      ? norm_backward_kernel<8, 1, F32>
            : lanes == 16   ? norm_backward_kernel<16, 1, F32>
            : lanes == 32   ? norm_backward_kernel<32, 1, F32>
-           : lanes == 64   ? (n <= 64 ? norm_backward_kernel<64, 1, F32>
-                                      : norm_backward_kernel<64, 2, F32>)
-           : lanes == 256  ? (n <= 256   ? norm_backward_kernel<256, 1, F32>
-                              : n <= 512 ? norm_backward_kernel<256, 2, F32>
-                                         : norm_backward_kernel<256, 3, F32>)
-           : lanes == 512  ? norm_backward_kernel<512, 2, F32>
+           : lanes == 64   ? norm_backward_kernel<64, 1, F32>
+           : lanes == 128  ? norm_backward_kernel<128, 1, F32>
+           : lanes == 256  ? norm_backward_kernel<256, 1, F32>
+           : lanes == 512  ? norm_backward_kernel<512, 1, F32>
+           : lanes == 768  ? norm_backward_kernel<768, 1, F32>
+           : n <= 1024     ? norm_backward_kernel<1024, 1, F32>
                            : norm_backward_kernel<1024, 2, F32>,
            dim3(backward_groups(n, g.T)), dim3(block_of(lanes)), 0, s, g);
 }

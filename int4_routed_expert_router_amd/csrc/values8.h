@@ -34,12 +34,16 @@ COLI_DEV void unpack8(const uint4 u, float v[8]) {
   }
 }
 
+// Two fp32 -> bf16, round to nearest even, by the hardware's conversion (one
+// instruction for what takes a dozen in integers).
+COLI_DEV uint32_t pack2(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const f32x2 v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, coli_bf16x2));
+}
+
 COLI_DEV uint4 pack8(const float v[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = f32_to_bf16_bits(v[2 * i]) | (f32_to_bf16_bits(v[2 * i + 1]) << 16);
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
 }
 
 // Values 8i .. 8i+7 of p.
