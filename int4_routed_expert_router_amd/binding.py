@@ -247,6 +247,16 @@ def _need(t, name, dtype, numel, dev):
                                         "" if t.is_contiguous() else " (strided)"))
 
 
+def _arg(t, name, dtype, numel, dev):
+    """The pointer of a tensor that `_need` takes, None for None."""
+    if t is None:
+        return None
+    if (t.dtype is dtype and t.get_device() == dev and t.numel() >= numel
+            and t.is_contiguous()):
+        return t.data_ptr()
+    return _need(t, name, dtype, numel, dev)
+
+
 class Adapters:
     """Low-rank adapters of one N x K matrix: a [n, R, K] and b [n, N, R] bf16
     on the device, R a multiple of 8 up to 128; rank [n] int32 and scale [n]
@@ -537,6 +547,8 @@ def coli_moe_route_backward(layer: Layer, logits, topk_idx, T: int, d_topk_w, ba
 
 
 _DTYPES = {torch.bfloat16: COLI_SRC_BF16, torch.float32: COLI_SRC_F32}
+# types of the codes and scales that coli_moe_norm writes
+_CODES = {COLI_NORM_Q8_0: (torch.int8, torch.float16), COLI_NORM_MXFP8: (torch.uint8, torch.uint8)}
 
 
 def _dtype(t, name):
@@ -583,20 +595,12 @@ def coli_moe_norm(norm: Norm, x, residual, total, T: int, y, fmt: int = COLI_NOR
     q int8 and scales fp16 for Q8_0, both uint8 for MXFP8."""
     n, dev = T * norm.hidden, x.get_device()
     _norm_weight(norm, dev, x)
-    _need(x, "x", torch.bfloat16, n, dev)
-    _need(y, "y", torch.bfloat16, n, dev)
-    rd = _dtype(residual, "residual")
-    if residual is not None:
-        _need(residual, "residual", residual.dtype, n, dev)
-        _need(total, "total", residual.dtype, n, dev)
-    if fmt == COLI_NORM_Q8_0:
-        _need(q, "q", torch.int8, n, dev)
-        _need(scales, "scales", torch.float16, n // 32, dev)
-    elif fmt == COLI_NORM_MXFP8:
-        _need(q, "q", torch.uint8, n, dev)
-        _need(scales, "scales", torch.uint8, n // 32, dev)
-    _run("coli_moe_norm", x, stream, ctypes.byref(norm.c), x.data_ptr(), _ptr(residual), rd, T,
-         _ptr(total), _ptr(y), fmt, _ptr(q), _ptr(scales))
+    rd, stype = _dtype(residual, "residual"), None if residual is None else residual.dtype
+    qt, st = _CODES.get(fmt, (None, None))
+    _run("coli_moe_norm", x, stream, ctypes.byref(norm.c), _arg(x, "x", torch.bfloat16, n, dev),
+         _arg(residual, "residual", stype, n, dev), rd, T, _arg(total, "total", stype, n, dev),
+         _arg(y, "y", torch.bfloat16, n, dev), fmt, _arg(q, "q", qt, n, dev),
+         _arg(scales, "scales", st, n // 32, dev))
 
 
 def coli_moe_norm_backward(norm: Norm, total, T: int, dy, d_total, dx, d_residual, d_weight,
@@ -604,80 +608,75 @@ def coli_moe_norm_backward(norm: Norm, total, T: int, dy, d_total, dx, d_residua
     """dx (bf16), d_residual (total's type) and d_weight (fp32) of coli_moe_norm
     from total (x where there was no residual); d_total and any of the outputs
     may be None, ws too without d_weight."""
-    n, dev = T * norm.hidden, total.get_device()
+    n, dev, td, stype = T * norm.hidden, total.get_device(), _dtype(total, "total"), total.dtype
     _norm_weight(norm, dev, total)
-    td = _dtype(total, "total")
-    _need(total, "total", total.dtype, n, dev)
-    _need(dy, "dy", torch.bfloat16, n, dev)
-    _need(d_total, "d_total", total.dtype, n, dev)
-    _need(dx, "dx", torch.bfloat16, n, dev)
-    _need(d_residual, "d_residual", total.dtype, n, dev)
-    _need(d_weight, "d_weight", torch.float32, norm.hidden, dev)
-    _run("coli_moe_norm_backward", total, stream, ctypes.byref(norm.c), total.data_ptr(), td,
-         dy.data_ptr(), _ptr(d_total), T, _ptr(dx), _ptr(d_residual), _ptr(d_weight),
+    _run("coli_moe_norm_backward", total, stream, ctypes.byref(norm.c),
+         _arg(total, "total", stype, n, dev), td, _arg(dy, "dy", torch.bfloat16, n, dev),
+         _arg(d_total, "d_total", stype, n, dev), T, _arg(dx, "dx", torch.bfloat16, n, dev),
+         _arg(d_residual, "d_residual", stype, n, dev),
+         _arg(d_weight, "d_weight", torch.float32, norm.hidden, dev),
          *((None, 0) if ws is None else _ws(ws, total)))
 
 
 def coli_moe_forward_prefill_quantized(layer: Layer, route: Route, q, scales, T: int, y,
                                        y_dtype: int, ws, stream=None):
     """coli_moe_forward_prefill of the codes that coli_moe_norm writes."""
-    dev, mx = q.get_device(), bool(layer.c.flags & COLI_ACT_MXFP8)
-    _need(q, "q", torch.uint8 if mx else torch.int8, T * layer.hidden, dev)
-    _need(scales, "scales", torch.uint8 if mx else torch.float16, T * layer.hidden // 32, dev)
-    _need(y, "y", torch.float32 if y_dtype == COLI_OUT_F32 else torch.bfloat16, T * layer.hidden,
-          dev)
+    dev, n = q.get_device(), T * layer.hidden
+    qt, st = _CODES[COLI_NORM_MXFP8 if layer.c.flags & COLI_ACT_MXFP8 else COLI_NORM_Q8_0]
     _need(route.topk_w, "route", torch.float32, T * layer.top_k, dev)
+    for w in (layer.q4, layer.scales):
+        if isinstance(w, torch.Tensor) and w.get_device() != dev:
+            raise ValueError("the layer's weights on %s, q on %s" % (w.device, q.device))
     _run("coli_moe_forward_prefill_quantized", q, stream, ctypes.byref(layer.c),
-         ctypes.byref(route.c), q.data_ptr(), scales.data_ptr(), T, y.data_ptr(), y_dtype,
-         *_ws(ws, q))
+         ctypes.byref(route.c), _arg(q, "q", qt, n, dev), _arg(scales, "scales", st, n // 32, dev),
+         T, _arg(y, "y", torch.float32 if y_dtype == COLI_OUT_F32 else torch.bfloat16, n, dev),
+         y_dtype, *_ws(ws, q))
 
 
-def _rows_args(layer, route, rows, beside, token, T):
-    """Device, types and rows of the calls on rows by expert: `rows` is a buffer
-    of rows, `token` and `beside` are by token."""
-    dev, h = rows.get_device(), layer.hidden
-    rd, td = _dtype(rows, "rows"), _dtype(token, "y")
-    _need(rows, "rows", rows.dtype, h, dev)
-    _need(token, "y", token.dtype, T * h, dev)
-    _need(beside, "beside", rows.dtype, T * h, dev)
+def _route_arg(layer, route, T, dev):
     _need(route.pair_pos, "route", torch.int32, T * layer.top_k, dev)
-    return rd, td, rows.numel() // h
+    return ctypes.byref(layer.c), ctypes.byref(route.c)
 
 
 def coli_moe_dispatch(layer: Layer, route: Route, x, T: int, rows, stream=None):
     """rows[pair_pos[t*k + j]] = x[t]; x and rows both bf16 or both fp32."""
-    rd, td, n = _rows_args(layer, route, rows, None, x, T)
-    if rd != td:
-        raise ValueError("x of %s, rows of %s" % (x.dtype, rows.dtype))
-    _run("coli_moe_dispatch", x, stream, ctypes.byref(layer.c), ctypes.byref(route.c),
-         x.data_ptr(), rd, T, rows.data_ptr(), n)
+    h, dev, dt = layer.hidden, rows.get_device(), _dtype(rows, "rows")
+    _run("coli_moe_dispatch", x, stream, *_route_arg(layer, route, T, dev),
+         _arg(x, "x", rows.dtype, T * h, dev), dt, T, _arg(rows, "rows", rows.dtype, h, dev),
+         rows.numel() // h)
+
+
+def _sum_rows(name, layer, route, rows, beside, T, out, stream):
+    h, dev = layer.hidden, rows.get_device()
+    rd, od = _dtype(rows, "rows"), _dtype(out, "y")
+    _run(name, out, stream, *_route_arg(layer, route, T, dev),
+         _arg(rows, "rows", rows.dtype, h, dev), rd, rows.numel() // h,
+         _arg(beside, "beside", rows.dtype, T * h, dev), T, _arg(out, "y", out.dtype, T * h, dev),
+         od)
 
 
 def coli_moe_dispatch_backward(layer: Layer, route: Route, d_rows, beside, T: int, dx,
                                stream=None):
     """dx[t] = sum over t's pairs of d_rows (+ beside, of d_rows' type, or None)."""
-    rd, td, n = _rows_args(layer, route, d_rows, beside, dx, T)
-    _run("coli_moe_dispatch_backward", dx, stream, ctypes.byref(layer.c), ctypes.byref(route.c),
-         d_rows.data_ptr(), rd, n, _ptr(beside), T, dx.data_ptr(), td)
+    _sum_rows("coli_moe_dispatch_backward", layer, route, d_rows, beside, T, dx, stream)
 
 
 def coli_moe_combine(layer: Layer, route: Route, rows, beside, T: int, y, stream=None):
     """y[t] = sum over t's pairs of topk_w * rows (+ beside, of rows' type, or None)."""
-    rd, td, n = _rows_args(layer, route, rows, beside, y, T)
-    _run("coli_moe_combine", y, stream, ctypes.byref(layer.c), ctypes.byref(route.c),
-         rows.data_ptr(), rd, n, _ptr(beside), T, y.data_ptr(), td)
+    _sum_rows("coli_moe_combine", layer, route, rows, beside, T, y, stream)
 
 
 def coli_moe_combine_backward(layer: Layer, route: Route, rows, dy, T: int, d_rows, d_topk_w,
                               stream=None):
     """d_rows (of rows' type) and d_topk_w (fp32) of coli_moe_combine; either may
     be None, and rows too without d_topk_w."""
-    rd, td, n = _rows_args(layer, route, d_rows if rows is None else rows, None, dy, T)
-    if rows is not None and d_rows is not None:
-        _need(d_rows, "d_rows", rows.dtype, n * layer.hidden, rows.get_device())
-    _need(d_topk_w, "d_topk_w", torch.float32, T * layer.top_k, dy.get_device())
-    _run("coli_moe_combine_backward", dy, stream, ctypes.byref(layer.c), ctypes.byref(route.c),
-         _ptr(rows), rd, n, dy.data_ptr(), td, T, _ptr(d_rows), _ptr(d_topk_w))
+    h, like = layer.hidden, d_rows if rows is None else rows
+    dev, rd, yd = like.get_device(), _dtype(like, "rows"), _dtype(dy, "dy")
+    n = like.numel() // h
+    _run("coli_moe_combine_backward", dy, stream, *_route_arg(layer, route, T, dev),
+         _arg(rows, "rows", like.dtype, h, dev), rd, n, _arg(dy, "dy", dy.dtype, T * h, dev), yd, T,
+         _arg(d_rows, "d_rows", like.dtype, n * h, dev),
+         _arg(d_topk_w, "d_topk_w", torch.float32, T * layer.top_k, dev))
 
 
 class Gradients:

@@ -326,7 +326,7 @@ def test_binding_refuses_wrong_tensors():
         coli.coli_moe_forward_prefill_quantized(L, r, q, sc, T, x, coli.COLI_OUT_BF16, ws)
     with FakeTensorMode():
         r.pair_pos = torch.empty(2 * T, dtype=torch.int32, device="cuda")
-    with pytest.raises(ValueError, match="x of"):
+    with pytest.raises(ValueError, match="x: expected"):
         coli.coli_moe_dispatch(L, r, res, T, rows)
     for t in bad:
         with pytest.raises(ValueError):
