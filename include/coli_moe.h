@@ -530,9 +530,10 @@ int coli_moe_balance_loss(const coli_moe_layer_t *layer, const float *logits,
  * flags and routed_scale, the choice of experts and the counts being
  * constants.
  *  d_topk_w [T*k] fp32 or NULL: for the layer's output y, dy[t] times the
- *  output of expert topk_idx[t][j] for row t.  The caller brings it: the
- *  forward calls add the experts' outputs up and return none of them alone
- *  (coli_moe_project computes one expert's projections).
+ *  output of expert topk_idx[t][j] for row t.  The forward calls add the
+ *  experts' outputs up and return none of them alone; where they are computed
+ *  expert by expert (coli_moe_dispatch, coli_moe_project, coli_moe_combine),
+ *  coli_moe_combine_backward gives it.
  *  balance (the buffers coli_moe_balance_loss filled for these logits) and
  *  d_loss [2] fp32, device: both given or both NULL.  At least one of the two
  *  parts is given.
@@ -597,7 +598,7 @@ size_t coli_moe_norm_workspace_bytes(const coli_moe_norm_t *norm, int32_t T);
  * d is the gradient of x and of residual alike.
  *  total, d_total [T*H] of total_dtype (COLI_SRC_*), dy [T*H] bf16; d_total,
  *  the gradient that reaches the stream past this layer, may be NULL;
- *  dx [T*H] bf16 or NULL (may be dy itself, or d_total of that type);
+ *  dx [T*H] bf16 or NULL (may be dy itself, or d_total if that is bf16);
  *  d_residual [T*H] of total_dtype or NULL (may be d_total itself; the same d
  *  as dx, for a stream of another type);  d_weight [H] fp32 or NULL, written
  *  whole.  At least one output is given.  T in [1, 2^24]; all 16-byte
@@ -626,7 +627,8 @@ int coli_moe_forward_prefill_quantized(const coli_moe_layer_t *layer,
  * offsets[e] .. offsets[e+1]).  A caller may write others: a pair whose
  * pair_pos is outside [0, n_rows) has no row (it went over an expert's limit,
  * or its expert is on another device); the rows of different pairs have to be
- * different.  Rows that no pair owns are neither read nor written.
+ * different.  Rows that no pair owns are not written, and what they hold does
+ * not matter.
  * These calls read route->pair_pos and, where stated, route->topk_w, and H, E
  * and k of `layer` (no weights).  T in [1, 65536], T*k <= 2^20, n_rows in
  * [1, 2^21].  Element types are COLI_SRC_BF16 or COLI_SRC_F32; sums are fp32,

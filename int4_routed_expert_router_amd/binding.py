@@ -633,9 +633,13 @@ def coli_moe_forward_prefill_quantized(layer: Layer, route: Route, q, scales, T:
          y_dtype, *_ws(ws, q))
 
 
-def _route_arg(layer, route, T, dev):
-    _need(route.pair_pos, "route", torch.int32, T * layer.top_k, dev)
-    return ctypes.byref(layer.c), ctypes.byref(route.c)
+def _route_arg(layer, route, T, dev, weights=False):
+    """The route's tensors as they are now: a caller may have put others in place."""
+    c, n = route.c, T * layer.top_k
+    c.pair_pos = _arg(route.pair_pos, "route", torch.int32, n, dev)
+    if weights:
+        c.topk_w = _arg(route.topk_w, "route", torch.float32, n, dev)
+    return ctypes.byref(layer.c), ctypes.byref(c)
 
 
 def coli_moe_dispatch(layer: Layer, route: Route, x, T: int, rows, stream=None):
@@ -649,7 +653,8 @@ def coli_moe_dispatch(layer: Layer, route: Route, x, T: int, rows, stream=None):
 def _sum_rows(name, layer, route, rows, beside, T, out, stream):
     h, dev = layer.hidden, rows.get_device()
     rd, od = _dtype(rows, "rows"), _dtype(out, "y")
-    _run(name, out, stream, *_route_arg(layer, route, T, dev),
+    _run(name, out, stream,
+         *_route_arg(layer, route, T, dev, name == "coli_moe_combine"),
          _arg(rows, "rows", rows.dtype, h, dev), rd, rows.numel() // h,
          _arg(beside, "beside", rows.dtype, T * h, dev), T, _arg(out, "y", out.dtype, T * h, dev),
          od)
@@ -673,7 +678,7 @@ def coli_moe_combine_backward(layer: Layer, route: Route, rows, dy, T: int, d_ro
     h, like = layer.hidden, d_rows if rows is None else rows
     dev, rd, yd = like.get_device(), _dtype(like, "rows"), _dtype(dy, "dy")
     n = like.numel() // h
-    _run("coli_moe_combine_backward", dy, stream, *_route_arg(layer, route, T, dev),
+    _run("coli_moe_combine_backward", dy, stream, *_route_arg(layer, route, T, dev, True),
          _arg(rows, "rows", like.dtype, h, dev), rd, n, _arg(dy, "dy", dy.dtype, T * h, dev), yd, T,
          _arg(d_rows, "d_rows", like.dtype, n * h, dev),
          _arg(d_topk_w, "d_topk_w", torch.float32, T * layer.top_k, dev))

@@ -524,6 +524,10 @@ int coli_moe_norm_backward(const coli_moe_norm_t *norm, const void *total, int32
   if (rc) return rc;
   if (!total || !is_dtype(total_dtype) || !dy || (!dx && !d_residual && !d_weight))
     return COLI_E_INVALID;
+  // dx over d_total or d_residual only if they are bf16 too, d_residual over dy likewise
+  if (total_dtype != COLI_SRC_BF16 &&
+      ((dx && (dx == d_total || dx == d_residual)) || (d_residual && d_residual == dy)))
+    return COLI_E_INVALID;
   if (!aligned(total, 16) || !aligned(dy, 16) || !aligned(d_total, 16) || !aligned(dx, 16) ||
       !aligned(d_residual, 16) || !aligned(d_weight, 16))
     return COLI_E_ALIGN;
@@ -550,7 +554,7 @@ int coli_moe_dispatch_backward(const coli_moe_layer_t *layer, const coli_moe_rou
   Layer L;
   const int rc = check_rows(layer, route, T, n_rows, rows_dtype, dx_dtype, false, &L);
   if (rc) return rc;
-  if (!d_rows || !dx) return COLI_E_INVALID;
+  if (!d_rows || !dx || (dx == beside && dx_dtype != rows_dtype)) return COLI_E_INVALID;
   if (!aligned(d_rows, 16) || !aligned(beside, 16) || !aligned(dx, 16)) return COLI_E_ALIGN;
   return launch_rows_combine(L, route->pair_pos, nullptr, d_rows, rows_dtype, n_rows, beside, T,
                              dx, dx_dtype, reinterpret_cast<hipStream_t>(stream));
@@ -562,7 +566,7 @@ int coli_moe_combine(const coli_moe_layer_t *layer, const coli_moe_route_t *rout
   Layer L;
   const int rc = check_rows(layer, route, T, n_rows, rows_dtype, y_dtype, true, &L);
   if (rc) return rc;
-  if (!rows || !y) return COLI_E_INVALID;
+  if (!rows || !y || (y == beside && y_dtype != rows_dtype)) return COLI_E_INVALID;
   if (!aligned(rows, 16) || !aligned(beside, 16) || !aligned(y, 16)) return COLI_E_ALIGN;
   return launch_rows_combine(L, route->pair_pos, route->topk_w, rows, rows_dtype, n_rows, beside,
                              T, y, y_dtype, reinterpret_cast<hipStream_t>(stream));

@@ -171,6 +171,19 @@ def test_scale(scale):
     _check(x, res, w, _run(x, res, w, eps=1e-30), eps=1e-30)
 
 
+def test_every_bf16_value():
+    """The stored sum for every finite bf16 x, subnormal ones among them, beside
+    nothing, a value of its own size and a tiny one."""
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(BF)
+    x = x[x.isfinite()].view(255, 256).cuda()
+    g = torch.Generator(device="cuda").manual_seed(6)
+    near = (x.float() * (torch.rand(x.shape, generator=g, device="cuda") * 2 - 1)).to(BF)
+    for res in (torch.zeros_like(x), near, torch.full_like(x, 1e-40)):
+        out = _run(x, res, None)
+        # -0 + 0 is +0 in both
+        assert torch.equal(out["total"].view(torch.int16), (x.float() + res.float()).to(BF).view(torch.int16))
+
+
 def test_many_rows():
     """More rows than a launch has workgroups, and buffers past 2 GiB."""
     g = torch.Generator(device="cuda").manual_seed(1)

@@ -173,6 +173,22 @@ def test_gradients_are_those_of_the_forward_calls():
         assert abs(float((got.double() * along).sum() - num)) <= 110 * H24 * absolute + 1e-9 * a
 
 
+def test_a_route_of_other_tensors():
+    """Positions and weights that the caller put in place of the route's own."""
+    c = Case(20, 256, 8, 2, seed=9)
+    x, y = c.new(20, F32), torch.empty(20, 256, device="cuda")
+    c.r.pair_pos = torch.randperm(40, generator=c.g, device="cuda").to(torch.int32)
+    c.r.topk_w = torch.rand(40, generator=c.g, device="cuda")
+    c.pos, c.w = c.r.pair_pos.long().view(20, 2), c.r.topk_w.view(20, 2)
+    c.has = torch.ones_like(c.has)
+    rows = torch.empty(40, 256, device="cuda")
+    coli.coli_moe_dispatch(c.L, c.r, x, 20, rows)
+    coli.coli_moe_combine(c.L, c.r, rows, None, 20, y)
+    torch.cuda.synchronize()
+    assert torch.equal(rows[c.pos], x[:, None, :].expand(20, 2, 256))
+    _check_sum(c, rows, c.w, None, y)
+
+
 def test_with_nothing_but_missing_pairs():
     c = Case(6, 256, 8, 2, drop=1.1)
     rows, b = c.new(c.n, BF), c.new(6, BF)

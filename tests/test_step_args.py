@@ -85,6 +85,11 @@ def test_norm_backward_refusals():
     assert norm_backward(nb=need - 1) == WORKSPACE
     for name in ("total", "dy", "d_total", "dx", "dr", "dw"):
         assert norm_backward(**{name: FAKE + 8}) == ALIGN
+    # outputs over inputs of another type
+    far = [FAKE + (i << 20) for i in range(1, 5)]
+    assert norm_backward(td=1, dy=far[0], d_total=far[1], dx=far[1], dr=far[2]) == INVALID
+    assert norm_backward(td=1, dy=far[0], d_total=far[1], dx=far[2], dr=far[2]) == INVALID
+    assert norm_backward(td=1, dy=far[0], d_total=far[1], dx=far[2], dr=far[0]) == INVALID
 
 
 def test_norm_workspace():
@@ -163,6 +168,9 @@ def test_rows_refusals(call):
         assert call(r=route(topk_w=FAKE + 1)) == ALIGN
     if call in (combine, dispatch_backward):
         assert call(beside=FAKE + 4) == ALIGN
+        # onto beside, of another type
+        assert call(dtype=1, other_dtype=0, beside=FAKE, other=FAKE) == INVALID
+        assert call(dtype=0, other_dtype=1, beside=FAKE, other=FAKE) == INVALID
 
 
 def test_combine_backward_outputs():
