@@ -675,7 +675,7 @@ int coli_moe_combine_backward(const coli_moe_layer_t *layer, const coli_moe_rout
  * One gradient and where its clipped values go; host memory.
  *  grad, out : device, n values each of their COLI_SRC_* types, aligned to the
  *              type.  out may be grad itself (same type); otherwise no out may
- *              overlap another out or any grad.  n in [0, 2^40]. */
+ *              overlap another out or any grad.  All n together at most 2^36. */
 typedef struct coli_moe_gradient {
   const void *grad;
   void *out;
@@ -713,7 +713,7 @@ size_t coli_moe_clip_workspace_bytes(void);
  *   out = grad * norm[1], rounded to out's type
  * An out that is its grad is not touched where norm[1] is 1.
  *  items [n_items] device, 8-byte aligned, from coli_moe_clip_plan (n_items
- *  may be 0: norm 0);  max_norm >= 0, infinity for the norm alone;  norm [2]
+ *  below 2^24; 0: norm 0);  max_norm >= 0, infinity for the norm alone;  norm [2]
  *  fp32, device. */
 int coli_moe_clip_gradients(const coli_moe_clip_item_t *items, int64_t n_items, float max_norm,
                             float *norm, void *ws, size_t ws_bytes, void *stream);

@@ -600,7 +600,7 @@ size_t coli_moe_clip_workspace_bytes(void) { return clip_workspace(); }
 
 int coli_moe_clip_gradients(const coli_moe_clip_item_t *items, int64_t n_items, float max_norm,
                             float *norm, void *ws, size_t ws_bytes, void *stream) {
-  if (n_items < 0 || (n_items && !items) || !norm || !(max_norm >= 0.0f)) return COLI_E_INVALID;
+  if (n_items < 0 || n_items >= (1 << 24) || (n_items && !items) || !norm || !(max_norm >= 0.0f)) return COLI_E_INVALID;
   if (!aligned(items, 8) || !aligned(norm, 4)) return COLI_E_ALIGN;
   const int rc = check_ws(ws, ws_bytes, clip_workspace());
   if (rc) return rc;

@@ -16,7 +16,7 @@ namespace coli {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kGroups = 1536;  // partial sums: six workgroups to a CU
+constexpr int kGroups = 1024;  // partial sums
 constexpr int kItem = 8192;    // values of an item, at most
 constexpr int kFew = 16;       // items that one workgroup takes alone, a wave each
 enum { kGradF32 = 1, kOutF32 = 2 };
@@ -97,7 +97,7 @@ COLI_DEV double item_squares(const void *g, int n, int tid) {
   return a;
 }
 
-template <bool F32, bool OF32, int THREADS>
+template <bool F32, bool OF32, int THREADS, bool NT>
 COLI_DEV void item_scale(const void *g, void *o, int n, float f, int tid) {
   constexpr int V = F32 ? 4 : 8;
   int head = head_of<F32>(g, n), body = (n - head) / V;
@@ -114,8 +114,9 @@ COLI_DEV void item_scale(const void *g, void *o, int n, float f, int tid) {
     if (OF32) {
 #pragma unroll
       for (int j = 0; j < V; j += 4)
-        reinterpret_cast<float4 *>(oat)[(V * i + j) / 4] =
-            make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        store16<NT>(reinterpret_cast<uint4 *>(oat) + (V * i + j) / 4,
+                    make_uint4(__float_as_uint(v[j]), __float_as_uint(v[j + 1]),
+                               __float_as_uint(v[j + 2]), __float_as_uint(v[j + 3])));
     } else if (F32) {
       reinterpret_cast<uint2 *>(oat)[i] =
           make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
@@ -123,14 +124,14 @@ COLI_DEV void item_scale(const void *g, void *o, int n, float f, int tid) {
       float w[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[j] = v[F32 ? 0 : j];
-      reinterpret_cast<uint4 *>(oat)[i] = pack8(w);
+      store16<NT>(reinterpret_cast<uint4 *>(oat) + i, pack8(w));
     }
   };
   int i0 = tid;
   for (; i0 - tid + kFlight * THREADS <= body; i0 += kFlight * THREADS) {
     uint4 u[kFlight];
 #pragma unroll
-    for (int c = 0; c < kFlight; ++c) u[c] = gat[i0 + c * THREADS];
+    for (int c = 0; c < kFlight; ++c) u[c] = load16<NT>(gat + i0 + c * THREADS);
 #pragma unroll
     for (int c = 0; c < kFlight; ++c) put(u[c], i0 + c * THREADS);
   }
@@ -153,14 +154,14 @@ COLI_DEV double squares_of(const coli_moe_clip_item_t &it, int tid) {
                               : item_squares<false, THREADS, NT>(it.grad, it.n, tid);
 }
 
-template <int THREADS>
+template <int THREADS, bool NT>
 COLI_DEV void scale(const coli_moe_clip_item_t &it, float f, int tid) {
   if (it.out == it.grad && f == 1.0f) return;
   switch (it.dtypes) {
-    case 0: item_scale<false, false, THREADS>(it.grad, it.out, it.n, f, tid); break;
-    case kGradF32: item_scale<true, false, THREADS>(it.grad, it.out, it.n, f, tid); break;
-    case kOutF32: item_scale<false, true, THREADS>(it.grad, it.out, it.n, f, tid); break;
-    default: item_scale<true, true, THREADS>(it.grad, it.out, it.n, f, tid); break;
+    case 0: item_scale<false, false, THREADS, NT>(it.grad, it.out, it.n, f, tid); break;
+    case kGradF32: item_scale<true, false, THREADS, NT>(it.grad, it.out, it.n, f, tid); break;
+    case kOutF32: item_scale<false, true, THREADS, NT>(it.grad, it.out, it.n, f, tid); break;
+    default: item_scale<true, true, THREADS, NT>(it.grad, it.out, it.n, f, tid); break;
   }
 }
 
@@ -200,14 +201,17 @@ __global__ void __launch_bounds__(kThreads) clip_norm_kernel(
   if (threadIdx.x == 0) parts[blockIdx.x] = a;
 }
 
+// One item to a workgroup: with the norm's grid, several to each, 656 MB take
+// 254 us instead of 222.
+template <bool NT>
 __global__ void __launch_bounds__(kThreads) clip_scale_kernel(
-    const coli_moe_clip_item_t *__restrict__ items, int64_t n_items,
-    const double *__restrict__ parts, int n_parts, float max_norm, float *__restrict__ norm) {
+    const coli_moe_clip_item_t *__restrict__ items, const double *__restrict__ parts, int n_parts,
+    float max_norm, float *__restrict__ norm) {
   __shared__ double red[kThreads / 64];
   double a = 0.0;
   for (int i = threadIdx.x; i < n_parts; i += kThreads) a += parts[i];
   const float f = factor(group_sum64<kThreads>(a, red), max_norm, norm);
-  for (int64_t i = blockIdx.x; i < n_items; i += gridDim.x) scale<kThreads>(items[i], f, threadIdx.x);
+  scale<kThreads, NT>(items[blockIdx.x], f, threadIdx.x);
 }
 
 // Both in one workgroup, for a few items: a wave to an item.  16 items take 6.8 us
@@ -222,10 +226,12 @@ __global__ void __launch_bounds__(64 * kFew) clip_few_kernel(
   if (wave < n_items) it = items[wave];
   const double a = wave < n_items ? squares_of<64, false>(it, lane) : 0.0;
   const float f = factor(group_sum64<64 * kFew>(a, red), max_norm, norm);
-  if (wave < n_items) scale<64>(it, f, lane);
+  if (wave < n_items) scale<64, false>(it, f, lane);
 }
 
 // --------------------------------------------------------------------- plan
+
+constexpr int64_t kMaxValues = int64_t(1) << 36;  // the items of one launch: below 2^24
 
 int64_t bytes_of(int dtype) { return dtype == COLI_SRC_F32 ? 4 : 2; }
 
@@ -234,7 +240,7 @@ int check_gradients(const coli_moe_gradient_t *g, int32_t n, int64_t *total) {
   *total = 0;
   for (int32_t i = 0; i < n; ++i) {
     const coli_moe_gradient_t &t = g[i];
-    if (t.n < 0 || t.n > (int64_t(1) << 40)) return COLI_E_INVALID;
+    if (t.n < 0 || t.n > kMaxValues) return COLI_E_INVALID;
     if ((t.grad_dtype != COLI_SRC_BF16 && t.grad_dtype != COLI_SRC_F32) ||
         (t.out_dtype != COLI_SRC_BF16 && t.out_dtype != COLI_SRC_F32))
       return COLI_E_INVALID;
@@ -245,7 +251,7 @@ int check_gradients(const coli_moe_gradient_t *g, int32_t n, int64_t *total) {
         reinterpret_cast<uintptr_t>(t.out) % bytes_of(t.out_dtype))
       return COLI_E_ALIGN;
     *total += t.n;
-    if (*total > int64_t(1) << 42) return COLI_E_INVALID;
+    if (*total > kMaxValues) return COLI_E_INVALID;
   }
   return COLI_OK;
 }
@@ -340,16 +346,20 @@ int launch_clip(const coli_moe_clip_item_t *items, int64_t n_items, float max_no
   const int64_t rounds = (n_items + kGroups - 1) / kGroups;
   const int grid = (int)((n_items + rounds - 1) / rounds);
   // From a quarter of the chip's last cache on the sum reads past it: 656 MB in
-  // 97 us instead of 141, 110 MB in 18 instead of 29.  Below, the second kernel
+  // 95 us instead of 141, 110 MB in 18 instead of 29.  Below, the second kernel
   // gains more by finding there what the first has read (18 MB: 13.2 us for
-  // both, 14.1 past it; 66 MB: 39 either way).
+  // both, 14.1 past it; 66 MB: 39 either way).  The second kernel reads and
+  // writes past it where the results would not stay there anyway (656 MB: 222 us
+  // instead of 233).
+  const int64_t most = n_items * kItem * 4;  // bytes, if fp32
   launch_k(COLI_K_CLIP_NORM,
-           n_items * kItem * 4 >= int64_t(64) << 20 ? clip_norm_kernel<true>
-                                                     : clip_norm_kernel<false>,
+           most >= int64_t(64) << 20 ? clip_norm_kernel<true> : clip_norm_kernel<false>,
            dim3(grid), dim3(kThreads), 0, s, items, n_items, parts);
   if (hipGetLastError() != hipSuccess) return COLI_E_HIP;
-  launch_k(COLI_K_CLIP_SCALE, clip_scale_kernel, dim3(grid), dim3(kThreads), 0, s, items, n_items,
-           (const double *)parts, grid, max_norm, norm);
+  launch_k(COLI_K_CLIP_SCALE,
+           most >= int64_t(256) << 20 ? clip_scale_kernel<true> : clip_scale_kernel<false>,
+           dim3((unsigned)n_items), dim3(kThreads), 0, s, items, (const double *)parts, grid,
+           max_norm, norm);
   return hip_status(hipGetLastError());
 }
 

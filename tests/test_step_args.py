@@ -218,7 +218,8 @@ def test_plan_refusals():
     f = _lib().coli_moe_clip_items
     assert f(None, 1) == INVALID and f(grads(), -1) == INVALID
     assert f(grads((FAKE, FAKE, 4, 1, 1)), (1 << 20) + 1) == INVALID
-    for g, rc in (((FAKE, FAKE, -1, 1, 1), INVALID), ((FAKE, FAKE, (1 << 40) + 1, 1, 1), INVALID),
+    assert plan((FAKE, FAKE, 1 << 35, 0, 0), (BIG, BIG, (1 << 35) + 1, 0, 0)) == INVALID
+    for g, rc in (((FAKE, FAKE, -1, 1, 1), INVALID), ((FAKE, FAKE, (1 << 36) + 1, 1, 1), INVALID),
                   ((None, FAKE, 4, 1, 1), INVALID), ((FAKE, None, 4, 1, 1), INVALID),
                   ((FAKE, FAKE, 4, 2, 2), INVALID), ((FAKE, FAKE, 4, 1, 0), INVALID),
                   ((FAKE + 2, FAKE, 4, 1, 1), ALIGN), ((FAKE, FAKE + 1, 4, 1, 0), ALIGN)):
@@ -280,6 +281,7 @@ def test_clip_refusals():
     need = _lib().coli_moe_clip_workspace_bytes()
     assert f(None, 1, 1.0, FAKE, FAKE, BIG, None) == INVALID
     assert f(FAKE, -1, 1.0, FAKE, FAKE, BIG, None) == INVALID
+    assert f(FAKE, 1 << 24, 1.0, FAKE, FAKE, BIG, None) == INVALID
     for m in (-1.0, NAN, -INF):
         assert f(FAKE, 1, m, FAKE, FAKE, BIG, None) == INVALID
     assert f(FAKE, 1, 1.0, None, FAKE, BIG, None) == INVALID
