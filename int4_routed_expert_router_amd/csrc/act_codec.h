@@ -15,32 +15,34 @@ COLI_DEV uint32_t mx8_exponent(float amax) {
   return amax > 0.0f ? (uint32_t)max(0, min(254, E)) : 0u;
 }
 
-// ---- blocks held by four neighbouring lanes, eight values each -------------
+// ---- blocks held by neighbouring lanes, N = 8 or 4 values each ---------------
 // Codes and scales are bit for bit those of the prefill path's quantisers,
 // which hold a block in one thread.
 
-// Maximum of a >= 0 over the four lanes of a quad (non-negative floats order
-// as their bit patterns do).
-COLI_DEV float quad_max(float a) {
-  uint32_t u = __float_as_uint(a);
-  u = max(u, (uint32_t)__builtin_amdgcn_mov_dpp((int)u, 0xB1, 0xf, 0xf, false));  // [1, 0, 3, 2]
-  u = max(u, (uint32_t)__builtin_amdgcn_mov_dpp((int)u, 0x4E, 0xf, 0xf, false));  // [2, 3, 0, 1]
-  return __uint_as_float(u);
+// Maximum of a >= 0 over aligned groups of 32 / N lanes, by DPP moves
+// (non-negative floats order as their bit patterns do).
+template <int CTRL>
+COLI_DEV uint32_t dpp_max(uint32_t u) {
+  return max(u, (uint32_t)__builtin_amdgcn_mov_dpp((int)u, CTRL, 0xf, 0xf, false));
 }
-
-COLI_DEV float block_max(const float v[8]) {
+template <int N>
+COLI_DEV float block_max(const float (&v)[N]) {
   float a = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(v[i]));
-  return quad_max(a);
+  for (int i = 0; i < N; ++i) a = fmaxf(a, fabsf(v[i]));
+  uint32_t u = dpp_max<0x4E>(dpp_max<0xB1>(__float_as_uint(a)));  // swap neighbours, then pairs
+  if (N == 4) u = dpp_max<0x141>(u);                              // mirror halves of 8
+  return __uint_as_float(u);
 }
 
 // Q8_0: d = max / 127, q = round half away from zero of v / d, both divisions
 // IEEE; 0 for an all-zero block.  Returns d as fp16 bits.
-COLI_DEV uint16_t q8_0_lane(const float v[8], uint32_t q[2]) {
+template <int N>
+COLI_DEV uint16_t q8_0_lane(const float (&v)[N], uint32_t (&q)[N / 4]) {
   const float a = block_max(v);
   const float d = __fdiv_rn(a, 127.0f);
-  q[0] = q[1] = 0u;
+#pragma unroll
+  for (int w = 0; w < N / 4; ++w) q[w] = 0u;
   if (a != 0.0f) {
     // 2 v / d = v / (d / 2), halves being exact: the divisor's reciprocal with
     // one Newton step, then a product and two exact-residual corrections per
@@ -53,7 +55,7 @@ COLI_DEV uint16_t q8_0_lane(const float v[8], uint32_t q[2]) {
     const float y0 = __builtin_amdgcn_rcpf(h);
     const float y = fmaf(fmaf(-h, y0, 1.0f), y0, y0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < N; ++i) {
       float t = v[i] * y;
       t = fmaf(fmaf(-h, t, v[i]), y, t);
       t = fmaf(fmaf(-h, t, v[i]), y, t);
@@ -71,16 +73,17 @@ COLI_DEV uint16_t q8_0_lane(const float v[8], uint32_t q[2]) {
 // below the smallest code) and the hardware conversion rounds as the format
 // asks; it does not saturate, so the values are clamped first (all that lie in
 // (448, 512) round to 448).  Returns E.
-COLI_DEV uint32_t mx8_lane(const float v[8], uint32_t q[2]) {
+template <int N>
+COLI_DEV uint32_t mx8_lane(const float (&v)[N], uint32_t (&q)[N / 4]) {
   const uint32_t E = mx8_exponent(block_max(v));
   const float f = __uint_as_float((254u - E) << 23);  // 2^(127 - E), E <= 247
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
+  for (int w = 0; w < N / 4; ++w) {
     float m[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       m[i] = __builtin_amdgcn_fmed3f(v[4 * w + i] * f, -448.0f, 448.0f);
-    int p = __builtin_amdgcn_cvt_pk_fp8_f32(m[0], m[1], 0, false);
+    const int p = __builtin_amdgcn_cvt_pk_fp8_f32(m[0], m[1], 0, false);
     q[w] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(m[2], m[3], p, true);
   }
   return E;

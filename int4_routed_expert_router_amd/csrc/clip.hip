@@ -10,7 +10,7 @@
 #include <algorithm>
 
 #include "internal.h"
-#include "values8.h"
+#include "units.h"
 
 namespace coli {
 namespace {
@@ -114,7 +114,7 @@ COLI_DEV void item_scale(const void *g, void *o, int n, float f, int tid) {
     if (OF32) {
 #pragma unroll
       for (int j = 0; j < V; j += 4)
-        store16<NT>(reinterpret_cast<uint4 *>(oat) + (V * i + j) / 4,
+        store16<NT && F32>(reinterpret_cast<uint4 *>(oat) + (V * i + j) / 4,
                     make_uint4(__float_as_uint(v[j]), __float_as_uint(v[j + 1]),
                                __float_as_uint(v[j + 2]), __float_as_uint(v[j + 3])));
     } else if (F32) {

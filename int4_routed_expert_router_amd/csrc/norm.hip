@@ -3,7 +3,7 @@
 #include "act_codec.h"
 #include "internal.h"
 #include "lanes.h"
-#include "values8.h"
+#include "units.h"
 
 namespace coli {
 namespace {
@@ -11,14 +11,18 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int block_of(int lanes) { return lanes > 64 ? lanes : kThreads; }
 
-COLI_DEV void weight8(const void *w, int f32, int i, float v[8]) {
+// Values of a lane's units: fours where the stream is fp32, else eights.
+constexpr int unit_of(bool f32) { return f32 ? 4 : 8; }
+
+template <int U>
+COLI_DEV void load_weight(const void *w, int f32, int i, float (&v)[U]) {
   if (!w) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 1.0f;
+    for (int j = 0; j < U; ++j) v[j] = 1.0f;
   } else if (f32) {
-    load8<true>(w, i, v);
+    unpack(load_unit<U, true, false>(w, i), v);
   } else {
-    load8<false>(w, i, v);
+    unpack(load_unit<U, false, false>(w, i), v);
   }
 }
 
@@ -32,97 +36,95 @@ struct NormArgs {
   uint16_t *y;
   uint8_t *q;
   void *scales;
-  int T, chunks;  // rows, and chunks of eight values in a row
+  int T, units;  // rows, and units of a row
   int weight_f32, format;
   float eps, inv_h;
 };
 
-// RES: 0 no residual, 1 bf16, 2 fp32.  A row is held by LPR lanes, NC chunks
-// of eight values each.
-template <int LPR, int NC, int RES, bool NT>
+// RES: 0 no residual, 1 bf16, 2 fp32.  A row is held by LPR lanes, NU units each.
+template <int LPR, int NU, int RES, bool NT>
 __global__ void __launch_bounds__(block_of(LPR)) norm_kernel(NormArgs g) {
+  constexpr int U = unit_of(RES == 2);
   constexpr int B = block_of(LPR), RPB = B / LPR;  // rows of a workgroup
   __shared__ float red[2][1][LPR > 64 ? LPR / 64 : 1];
   const int li = threadIdx.x % LPR;
   int turn = 0;
   for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR; row < g.T;
        row += (int64_t)gridDim.x * RPB, turn ^= 1) {
-    const int64_t base = row * g.chunks;
-    float v[NC][8];
+    const int64_t base = row * g.units;
+    float v[NU][U];
     float sum[1] = {0.0f};
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
+    for (int c = 0; c < NU; ++c) {
       const int i = li + c * LPR;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[c][j] = 0.0f;
-      if (i < g.chunks) {
-        unpack8(load16<NT>(reinterpret_cast<const uint4 *>(g.x) + base + i), v[c]);
+      for (int j = 0; j < U; ++j) v[c][j] = 0.0f;
+      if (i < g.units) {
+        unpack(load_unit<U, false, NT>(g.x, base + i), v[c]);
         if (RES) {
-          float r[8];
-          if (RES == 1)
-            unpack8(load16<NT>(reinterpret_cast<const uint4 *>(g.residual) + base + i), r);
-          else
-            load8<true>(g.residual, base + i, r);
+          float r[U];
+          unpack(load_unit<U, RES == 2, NT>(g.residual, base + i), r);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[c][j] += r[j];
-          if (RES == 1) {  // the stored sum is what is normed
-            const uint4 p = pack8(v[c]);
-            store16<NT>(reinterpret_cast<uint4 *>(g.total) + base + i, p);
-            unpack8(p, v[c]);
-          } else {
-            store8<true>(g.total, base + i, v[c]);
-          }
+          for (int j = 0; j < U; ++j) v[c][j] += r[j];
+          const auto p = pack<U, RES == 2>(v[c]);
+          store_unit<U, RES == 2, NT>(g.total, base + i, p);
+          unpack(p, v[c]);  // the stored sum is what is normed
         }
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[0] = fmaf(v[c][j], v[c][j], sum[0]);
+      for (int j = 0; j < U; ++j) sum[0] = fmaf(v[c][j], v[c][j], sum[0]);
     }
     row_sums<LPR, 1>(sum, red[turn]);
     const float r = rsqrtf(fmaf(sum[0], g.inv_h, g.eps));
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
+    for (int c = 0; c < NU; ++c) {
       const int i = li + c * LPR;
-      if (i >= g.chunks) continue;  // with codes, whole quads of lanes
-      float w[8];
-      weight8(g.weight, g.weight_f32, i, w);
+      if (i >= g.units) continue;  // with codes, whole blocks of lanes
+      float w[U];
+      load_weight(g.weight, g.weight_f32, i, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] *= v[c][j] * r;
-      const uint4 p = pack8(w);
-      if (g.y) store16<NT>(reinterpret_cast<uint4 *>(g.y) + base + i, p);
+      for (int j = 0; j < U; ++j) w[j] *= v[c][j] * r;
+      const auto p = pack<U, false>(w);
+      if (g.y) store_unit<U, false, NT>(g.y, base + i, p);
       if (g.format != COLI_NORM_PLAIN) {
-        uint32_t q[2];
-        unpack8(p, w);
+        uint32_t q[U / 4];
+        constexpr int L = 32 / U;  // lanes of a block
+        unpack(p, w);
         if (g.format == COLI_NORM_Q8_0) {
           const uint16_t d = q8_0_lane(w, q);
-          if ((i & 3) == 0) reinterpret_cast<uint16_t *>(g.scales)[(base + i) >> 2] = d;
+          if (i % L == 0) reinterpret_cast<uint16_t *>(g.scales)[(base + i) / L] = d;
         } else {
           const uint32_t e = mx8_lane(w, q);
-          if ((i & 3) == 0) reinterpret_cast<uint8_t *>(g.scales)[(base + i) >> 2] = (uint8_t)e;
+          if (i % L == 0) reinterpret_cast<uint8_t *>(g.scales)[(base + i) / L] = (uint8_t)e;
         }
-        reinterpret_cast<uint2 *>(g.q)[base + i] = make_uint2(q[0], q[1]);
+        uint32_t *to = reinterpret_cast<uint32_t *>(g.q) + (base + i) * (U / 4);
+        if (U == 8)
+          *reinterpret_cast<uint2 *>(to) = make_uint2(q[0], q[U / 4 - 1]);
+        else
+          *to = q[0];
       }
     }
   }
 }
 
+// NC: chunks of eight values to a lane.
 template <int RES, int LPR, int NC>
 void run_norm(const NormArgs &g, hipStream_t s) {
-  constexpr int B = block_of(LPR), RPB = B / LPR;
+  constexpr int B = block_of(LPR), RPB = B / LPR, U = unit_of(RES == 2), NU = NC * 8 / U;
   const int64_t blocks = ((int64_t)g.T + RPB - 1) / RPB;
-  // From half as much again as the last cache on, all of bf16 x, residual, total
-  // and y go past it: 8,192 x 6144 in 69 us instead of 76, and 172 instead of
-  // 178 with a reader of y behind; 16,384 x 2048 (268 MB) 44 against 41.  fp32
-  // streams are left alone: their 16-byte halves of 32 cost more that way
-  // (16,384 x 6144: 242 against 225).
-  const int64_t bytes = (int64_t)g.T * g.chunks * (RES ? 64 : 32);
-  const bool nt = RES != 2 && bytes >= int64_t(384) << 20;
-  launch_k(COLI_K_NORM, nt ? norm_kernel<LPR, NC, RES, RES != 2> : norm_kernel<LPR, NC, RES, false>,
+  // From half as much again as the last cache on, x, residual, total and y go
+  // past it: 8,192 x 6144 in 69 us instead of 76, and 172 instead of 178 with a
+  // reader of y behind; 16,384 x 2048 (268 MB) 44 against 41.
+  const int64_t bytes = (int64_t)g.T * g.units * U * (RES == 2 ? 12 : RES ? 8 : 4);
+  launch_k(COLI_K_NORM,
+           bytes >= int64_t(384) << 20 ? norm_kernel<LPR, NU, RES, true>
+                                       : norm_kernel<LPR, NU, RES, false>,
            dim3((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20))), dim3(B), 0, s, g);
 }
 
 template <int RES>
 void pick_norm(const NormArgs &g, hipStream_t s) {
-  const int n = g.chunks;
+  const int n = g.units * unit_of(RES == 2) / 8;
   if (n <= 8) return run_norm<RES, 8, 1>(g, s);
   if (n <= 16) return run_norm<RES, 16, 1>(g, s);
   if (n <= 32) return run_norm<RES, 32, 1>(g, s);
@@ -145,85 +147,73 @@ struct NormBackArgs {
   uint16_t *dx;
   void *d_residual;
   float *parts;  // [gridDim.x][H] or NULL
-  int T, chunks;
+  int T, units;
   int weight_f32;
   float eps, inv_h;
 };
 
 // One lane's share of a row, as loaded.
-template <int NC, bool F32>
+template <int NU, bool F32>
 struct BackRow {
-  uint4 s[NC][F32 ? 2 : 1], o[NC][F32 ? 2 : 1], dy[NC];
+  Unit<unit_of(F32), F32> s[NU], o[NU];
+  Unit<unit_of(F32), false> dy[NU];
 };
 
-template <int LPR, int NC, bool F32>
-COLI_DEV void load_row(const NormBackArgs &g, int64_t row, int li, BackRow<NC, F32> &r) {
-  constexpr int U = F32 ? 2 : 1;
-  const int64_t base = row * g.chunks;
-  const uint4 *s = reinterpret_cast<const uint4 *>(g.total) + base * U;
-  const uint4 *o = reinterpret_cast<const uint4 *>(g.d_total) + base * U;
-  const uint4 *dy = reinterpret_cast<const uint4 *>(g.dy) + base;
+template <int LPR, int NU, bool F32, bool NT>
+COLI_DEV void load_row(const NormBackArgs &g, int64_t row, int li, BackRow<NU, F32> &r) {
+  constexpr int U = unit_of(F32);
+  const int64_t base = row * g.units;
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
+  for (int c = 0; c < NU; ++c) {
     const int i = li + c * LPR;
-    const bool in = row < g.T && i < g.chunks;
-    r.dy[c] = in ? dy[i] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      r.s[c][u] = in ? s[U * i + u] : make_uint4(0, 0, 0, 0);
-      r.o[c][u] = in && g.d_total ? o[U * i + u] : make_uint4(0, 0, 0, 0);
+    r.s[c] = r.o[c] = {};
+    r.dy[c] = {};
+    if (row < g.T && i < g.units) {
+      r.s[c] = load_unit<U, F32, NT>(g.total, base + i);
+      r.dy[c] = load_unit<U, false, NT>(g.dy, base + i);
+      if (g.d_total) r.o[c] = load_unit<U, F32, NT>(g.d_total, base + i);
     }
-  }
-}
-
-template <bool F32>
-COLI_DEV void unpack(const uint4 (&u)[F32 ? 2 : 1], float v[8]) {
-  if (F32) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint4 w = u[F32 ? j : 0];
-      v[4 * j] = __uint_as_float(w.x);
-      v[4 * j + 1] = __uint_as_float(w.y);
-      v[4 * j + 2] = __uint_as_float(w.z);
-      v[4 * j + 3] = __uint_as_float(w.w);
-    }
-  } else {
-    unpack8(u[0], v);
   }
 }
 
 // d = r (n - h mean(n h)) + d_total with h = s r: both row sums, of s^2 and of
 // n s, come from the one pass that loads the row.  A workgroup goes over rows
-// with the next one's loads in flight, and keeps its part of d_weight in
-// registers.
-template <int LPR, int NC, bool F32>
+// with the next one's loads in flight (up to 8192 values), and keeps its part
+// of d_weight in registers.
+template <int LPR, int NU, bool F32, bool NT>
 __global__ void __launch_bounds__(block_of(LPR)) norm_backward_kernel(NormBackArgs g) {
+  constexpr int U = unit_of(F32);
   constexpr int B = block_of(LPR), RPB = B / LPR;  // rows of a workgroup
   __shared__ float red[2][2][LPR > 64 ? LPR / 64 : 1];
   const int li = threadIdx.x % LPR, ri = threadIdx.x / LPR;
-  float dw[NC][8];
+  float dw[NU][U];
 #pragma unroll
-  for (int c = 0; c < NC; ++c)
+  for (int c = 0; c < NU; ++c)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[c][j] = 0.0f;
+    for (int j = 0; j < U; ++j) dw[c][j] = 0.0f;
   const int64_t step = (int64_t)gridDim.x * RPB;
   int64_t row = (int64_t)blockIdx.x * RPB + ri;
-  BackRow<NC, F32> a;
-  load_row<LPR>(g, row, li, a);
+  // two chunks to a lane leave no registers for a second row (fp32 4,096 x 16,384:
+  // 218 us, with it 272)
+  constexpr bool kAhead = NU * U == 8;
+  BackRow<NU, F32> a, next;
+  if (kAhead) load_row<LPR, NU, F32, NT>(g, row, li, a);
   int turn = 0;
   for (; row < g.T; row += step, turn ^= 1) {
-    BackRow<NC, F32> next;
-    load_row<LPR>(g, row + step, li, next);
+    if (kAhead)
+      load_row<LPR, NU, F32, NT>(g, row + step, li, next);
+    else
+      load_row<LPR, NU, F32, NT>(g, row, li, a);
     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
+    for (int c = 0; c < NU; ++c) {
       const int i = li + c * LPR;
-      float v[8], dy[8], w[8];
-      unpack<F32>(a.s[c], v);
-      unpack8(a.dy[c], dy);
-      weight8(i < g.chunks ? g.weight : nullptr, g.weight_f32, i, w);
+      float v[U], dy[U], w[U];
+      unpack(a.s[c], v);
+      unpack(a.dy[c], dy);
+      load_weight(i < g.units ? g.weight : nullptr, g.weight_f32, i, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < U; ++j) {
         sum[0] = fmaf(v[j], v[j], sum[0]);
         sum[1] = fmaf(dy[j] * w[j], v[j], sum[1]);
       }
@@ -231,48 +221,50 @@ __global__ void __launch_bounds__(block_of(LPR)) norm_backward_kernel(NormBackAr
     row_sums<LPR, 2>(sum, red[turn]);
     const float r = rsqrtf(fmaf(sum[0], g.inv_h, g.eps));
     const float m = sum[1] * g.inv_h * r;  // mean(n h)
-    const int64_t base = row * g.chunks;
+    const int64_t base = row * g.units;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
+    for (int c = 0; c < NU; ++c) {
       const int i = li + c * LPR;
-      if (i >= g.chunks) continue;
-      float v[8], dy[8], o[8], w[8], d[8];
-      unpack<F32>(a.s[c], v);
-      unpack<F32>(a.o[c], o);
-      unpack8(a.dy[c], dy);
-      weight8(g.weight, g.weight_f32, i, w);
+      if (i >= g.units) continue;
+      float v[U], dy[U], o[U], w[U], d[U];
+      unpack(a.s[c], v);
+      unpack(a.o[c], o);
+      unpack(a.dy[c], dy);
+      load_weight(g.weight, g.weight_f32, i, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < U; ++j) {
         const float h = v[j] * r;
         dw[c][j] = fmaf(dy[j], h, dw[c][j]);
         d[j] = fmaf(r, fmaf(-h, m, dy[j] * w[j]), o[j]);
       }
-      if (g.dx) store8<false>(g.dx, base + i, d);
-      if (g.d_residual) store8<F32>(g.d_residual, base + i, d);
+      if (g.dx) store_unit<U, false, NT>(g.dx, base + i, pack<U, false>(d));
+      if (g.d_residual) store_unit<U, F32, NT>(g.d_residual, base + i, pack<U, F32>(d));
     }
-    a = next;
+    if (kAhead) a = next;
   }
   if (!g.parts) return;
   if (RPB == 1) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
+    for (int c = 0; c < NU; ++c) {
       const int i = li + c * LPR;
-      if (i < g.chunks) store8<true>(g.parts, (int64_t)blockIdx.x * g.chunks + i, dw[c]);
+      if (i < g.units)
+        store_unit<U, true, false>(g.parts, (int64_t)blockIdx.x * g.units + i, pack<U, true>(dw[c]));
     }
     return;
   }
   // the rows of a workgroup that went side by side
-  __shared__ float side[RPB > 1 ? RPB : 1][RPB > 1 ? LPR * NC * 8 : 1];
+  __shared__ float side[RPB > 1 ? RPB : 1][RPB > 1 ? LPR * NU * U : 1];
 #pragma unroll
-  for (int c = 0; c < NC; ++c)
+  for (int c = 0; c < NU; ++c)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) side[RPB > 1 ? ri : 0][RPB > 1 ? 8 * (li + c * LPR) + j : 0] = dw[c][j];
+    for (int j = 0; j < U; ++j)
+      side[RPB > 1 ? ri : 0][RPB > 1 ? U * (li + c * LPR) + j : 0] = dw[c][j];
   __syncthreads();
-  for (int c = threadIdx.x; c < 8 * g.chunks; c += B) {
+  for (int c = threadIdx.x; c < U * g.units; c += B) {
     float sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < RPB; ++k) sum += side[k][RPB > 1 ? c : 0];
-    g.parts[(int64_t)blockIdx.x * 8 * g.chunks + c] = sum;
+    g.parts[(int64_t)blockIdx.x * U * g.units + c] = sum;
   }
 }
 
@@ -335,21 +327,34 @@ int backward_groups(int chunks, int T) {
   return groups < most ? groups : most;
 }
 
+template <int LPR, int NC, bool F32>
+void run_norm_backward(const NormBackArgs &g, hipStream_t s) {
+  constexpr int U = unit_of(F32), NU = NC * 8 / U;
+  const int chunks = g.units * U / 8;
+  // From three times the last cache on, rows go past it: 65,536 x 2048 in 204 us
+  // instead of 213, fp32 8,192 x 8192 199 instead of 208; at 403 MB the same.
+  const bool nt = (int64_t)g.T * g.units * U * (F32 ? 16 : 8) >= int64_t(768) << 20;
+  launch_k(COLI_K_NORM_BACKWARD,
+           nt ? norm_backward_kernel<LPR, NU, F32, true> : norm_backward_kernel<LPR, NU, F32, false>,
+           dim3(backward_groups(chunks, g.T)), dim3(block_of(LPR)), 0, s, g);
+}
+
 template <bool F32>
 void pick_norm_backward(const NormBackArgs &g, hipStream_t s) {
-  const int n = g.chunks, lanes = backward_lanes(n);
-  launch_k(COLI_K_NORM_BACKWARD,
-           lanes == 8      ? norm_backward_kernel<8, 1, F32>
-           : lanes == 16   ? norm_backward_kernel<16, 1, F32>
-           : lanes == 32   ? norm_backward_kernel<32, 1, F32>
-           : lanes == 64   ? norm_backward_kernel<64, 1, F32>
-           : lanes == 128  ? norm_backward_kernel<128, 1, F32>
-           : lanes == 256  ? norm_backward_kernel<256, 1, F32>
-           : lanes == 512  ? norm_backward_kernel<512, 1, F32>
-           : lanes == 768  ? norm_backward_kernel<768, 1, F32>
-           : n <= 1024     ? norm_backward_kernel<1024, 1, F32>
-                           : norm_backward_kernel<1024, 2, F32>,
-           dim3(backward_groups(n, g.T)), dim3(block_of(lanes)), 0, s, g);
+  const int chunks = g.units * unit_of(F32) / 8;
+  switch (backward_lanes(chunks)) {
+    case 8: return run_norm_backward<8, 1, F32>(g, s);
+    case 16: return run_norm_backward<16, 1, F32>(g, s);
+    case 32: return run_norm_backward<32, 1, F32>(g, s);
+    case 64: return run_norm_backward<64, 1, F32>(g, s);
+    case 128: return run_norm_backward<128, 1, F32>(g, s);
+    case 256: return run_norm_backward<256, 1, F32>(g, s);
+    case 512: return run_norm_backward<512, 1, F32>(g, s);
+    case 768: return run_norm_backward<768, 1, F32>(g, s);
+    default:
+      return chunks <= 1024 ? run_norm_backward<1024, 1, F32>(g, s)
+                            : run_norm_backward<1024, 2, F32>(g, s);
+  }
 }
 
 }  // namespace
@@ -370,7 +375,7 @@ int launch_norm(const coli_moe_norm_t &n, const uint16_t *x, const void *residua
   g.q = reinterpret_cast<uint8_t *>(q);
   g.scales = scales;
   g.T = T;
-  g.chunks = n.hidden / 8;
+  g.units = n.hidden / unit_of(residual && residual_dtype == COLI_SRC_F32);
   g.weight_f32 = n.weight_dtype == COLI_SRC_F32;
   g.format = format;
   g.eps = n.eps;
@@ -396,7 +401,7 @@ int launch_norm_backward(const coli_moe_norm_t &n, const void *total, int total_
   g.d_residual = d_residual;
   g.parts = d_weight ? reinterpret_cast<float *>(ws) : nullptr;
   g.T = T;
-  g.chunks = n.hidden / 8;
+  g.units = n.hidden / unit_of(total_dtype == COLI_SRC_F32);
   g.weight_f32 = n.weight_dtype == COLI_SRC_F32;
   g.eps = n.eps;
   g.inv_h = 1.0f / (float)n.hidden;
@@ -409,7 +414,7 @@ int launch_norm_backward(const coli_moe_norm_t &n, const void *total, int total_
   const int H = n.hidden;
   launch_k(COLI_K_NORM_REDUCE, H <= 2048 ? norm_reduce_kernel<16> : norm_reduce_kernel<64>,
            dim3(H <= 2048 ? (H + 15) / 16 : (H + 63) / 64), dim3(1024), 0, s, (const float *)ws,
-           backward_groups(g.chunks, T), H, d_weight);
+           backward_groups(H / 8, T), H, d_weight);
   return hip_status(hipGetLastError());
 }
 

@@ -8,7 +8,7 @@
 #include "device_common.h"
 #include "internal.h"
 #include "lanes.h"
-#include "values8.h"
+#include "units.h"
 
 namespace coli {
 namespace {
@@ -26,24 +26,24 @@ struct RowArgs {
   void *out_token;     // y or dx
   float *d_w;
   int64_t n_rows;
-  int T, k, chunks;    // chunks of a row: 16 bytes (dispatch) or 8 values
+  int T, k, units;     // units of a row: 16 bytes (dispatch), or 4 or 8 values
   int out_f32;         // type of out_token
 };
 
-// Which chunk of which token a thread of the kernels without a row sum takes:
-// LPR lanes to a token (256: as many workgroups as its chunks need), several
+// Which unit of which token a thread of the kernels without a row sum takes:
+// LPR lanes to a token (256: as many workgroups as its units need), several
 // tokens of short rows to a workgroup.
 template <int LPR>
-COLI_DEV bool my_chunk(const RowArgs &g, int &t, int &i) {
+COLI_DEV bool my_unit(const RowArgs &g, int &t, int &i) {
   if (LPR == kThreads) {  // the token is the same for the whole workgroup
-    const int per = (g.chunks + kThreads - 1) / kThreads;
+    const int per = (g.units + kThreads - 1) / kThreads;
     t = blockIdx.x / per;
     i = (blockIdx.x - t * per) * kThreads + threadIdx.x;
   } else {
     t = blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
     i = threadIdx.x % LPR;
   }
-  return t < g.T && i < g.chunks;
+  return t < g.T && i < g.units;
 }
 
 // ----------------------------------------------------------------- dispatch
@@ -51,8 +51,8 @@ COLI_DEV bool my_chunk(const RowArgs &g, int &t, int &i) {
 template <int LPR, bool NT>
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(RowArgs g) {
   int t, i;
-  if (!my_chunk<LPR>(g, t, i)) return;
-  const uint4 v = reinterpret_cast<const uint4 *>(g.token)[(int64_t)t * g.chunks + i];
+  if (!my_unit<LPR>(g, t, i)) return;
+  const uint4 v = reinterpret_cast<const uint4 *>(g.token)[(int64_t)t * g.units + i];
   const int32_t *pos = g.pos + (int64_t)t * g.k;
   for (int j0 = 0; j0 < g.k; j0 += kBatch) {
     int p[kBatch];
@@ -61,91 +61,67 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(RowArgs g) {
 #pragma unroll
     for (int j = 0; j < kBatch; ++j)
       if (p[j] >= 0 && p[j] < g.n_rows)
-        store16<NT>(reinterpret_cast<uint4 *>(g.out_rows) + (int64_t)p[j] * g.chunks + i, v);
+        store16<NT>(reinterpret_cast<uint4 *>(g.out_rows) + (int64_t)p[j] * g.units + i, v);
   }
 }
 
 // ------------------------------------------------------------------ combine
 
-// Eight values as loaded.
-template <bool F32>
-struct Raw8 {
-  uint4 u[F32 ? 2 : 1];
-};
-template <bool F32, bool NT = false>
-COLI_DEV Raw8<F32> raw8(const void *p, int64_t i) {
-  Raw8<F32> r;
-  const uint4 *at = reinterpret_cast<const uint4 *>(p) + i * (F32 ? 2 : 1);
-#pragma unroll
-  for (int h = 0; h < (F32 ? 2 : 1); ++h) r.u[h] = load16<NT>(at + h);
-  return r;
-}
-template <bool F32>
-COLI_DEV void values8(const Raw8<F32> &r, float v[8]) {
-  if (F32) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint4 w = r.u[F32 ? h : 0];
-      v[4 * h] = __uint_as_float(w.x);
-      v[4 * h + 1] = __uint_as_float(w.y);
-      v[4 * h + 2] = __uint_as_float(w.z);
-      v[4 * h + 3] = __uint_as_float(w.w);
-    }
-  } else {
-    unpack8(r.u[0], v);
-  }
-}
+// Values of a lane's units: fours of fp32 rows, eights of bf16 ones.
+constexpr int unit_of(bool f32) { return f32 ? 4 : 8; }
 
 // A batch of a token's rows is requested before the first is used.
 template <int LPR, bool F32, bool WEIGHTED, bool NT>
 __global__ void __launch_bounds__(kThreads) rows_combine_kernel(RowArgs g) {
+  constexpr int U = unit_of(F32);
   int t, i;
-  if (!my_chunk<LPR>(g, t, i)) return;
-  const int64_t own = (int64_t)t * g.chunks + i;
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  Raw8<F32> beside{};
-  if (g.token) beside = raw8<F32>(g.token, own);
+  if (!my_unit<LPR>(g, t, i)) return;
+  const int64_t own = (int64_t)t * g.units + i;
+  float acc[U], f[U];
+#pragma unroll
+  for (int e = 0; e < U; ++e) acc[e] = 0.0f;
+  Unit<U, F32> beside{};
+  if (g.token) beside = load_unit<U, F32, false>(g.token, own);
   for (int j0 = 0; j0 < g.k; j0 += kBatch) {
     bool has[kBatch];
     float w[kBatch];
-    Raw8<F32> v[kBatch];
+    Unit<U, F32> v[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       const int64_t p = (int64_t)t * g.k + j0 + j;
       const int r = j0 + j < g.k ? g.pos[p] : -1;
       has[j] = r >= 0 && r < g.n_rows;
       w[j] = WEIGHTED && has[j] ? g.w[p] : 1.0f;
-      v[j] = Raw8<F32>{};
-      if (has[j]) v[j] = raw8<F32, NT>(g.rows, (int64_t)r * g.chunks + i);
+      v[j] = {};
+      if (has[j]) v[j] = load_unit<U, F32, NT>(g.rows, (int64_t)r * g.units + i);
     }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       if (!has[j]) continue;
-      float f[8];
-      values8<F32>(v[j], f);
+      unpack(v[j], f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmaf(w[j], f[e], acc[e]);
+      for (int e = 0; e < U; ++e) acc[e] = fmaf(w[j], f[e], acc[e]);
     }
   }
   if (g.token) {
-    float f[8];
-    values8<F32>(beside, f);
+    unpack(beside, f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] += f[e];
+    for (int e = 0; e < U; ++e) acc[e] += f[e];
   }
   if (g.out_f32)
-    store8<true>(g.out_token, own, acc);
+    store_unit<U, true, false>(g.out_token, own, pack<U, true>(acc));
   else
-    store8<false>(g.out_token, own, acc);
+    store_unit<U, false, false>(g.out_token, own, pack<U, false>(acc));
 }
 
 // ----------------------------------------------------------------- backward
 
-// LPR lanes hold a token's dy, NC chunks of eight values each, while the rows
+// LPR lanes hold a token's dy, NU units each, while the rows
 // of its pairs pass, a batch of them in flight.  With few tokens their pairs
 // are spread over gridDim.y workgroups.  F32: type of the rows, DF32 of dy.
-template <int LPR, int NC, bool F32, bool DF32>
+template <int LPR, int NU, bool F32, bool DF32>
 __global__ void __launch_bounds__(block_of(LPR)) combine_backward_kernel(RowArgs g) {
+  constexpr int U = unit_of(F32);
   constexpr int B = block_of(LPR), W = LPR > 64 ? LPR / 64 : 1;
   // Rows of a batch: two, and more waves instead (2,051 x 6 of 2048: 17.4 us,
   // with one row 19.1, with eight 20.4; 65,536 x 2 of 256: 36, 38, 43).
@@ -156,18 +132,18 @@ __global__ void __launch_bounds__(block_of(LPR)) combine_backward_kernel(RowArgs
   const int per = (g.k + gridDim.y - 1) / gridDim.y;
   const int first = blockIdx.y * per, last = min(g.k, first + per);
   if (LPR <= 64 && t >= g.T) return;  // whole rows of lanes; no barrier follows
-  Raw8<DF32> dy[NC];
+  Unit<U, DF32> dy[NU];
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
+  for (int c = 0; c < NU; ++c) {
     const int i = li + c * LPR;
-    dy[c] = Raw8<DF32>{};
-    if (i < g.chunks) dy[c] = raw8<DF32>(g.token, (int64_t)t * g.chunks + i);
+    dy[c] = {};
+    if (i < g.units) dy[c] = load_unit<U, DF32, false>(g.token, (int64_t)t * g.units + i);
   }
   const int64_t pair = (int64_t)t * g.k;
   for (int j0 = first; j0 < last; j0 += JB) {
     int row[JB];
     float w[JB], dot[JB];
-    Raw8<F32> v[JB][NC];
+    Unit<U, F32> v[JB][NU];
 #pragma unroll
     for (int j = 0; j < JB; ++j) {
       const int r = j0 + j < last ? g.pos[pair + j0 + j] : -1;
@@ -175,34 +151,34 @@ __global__ void __launch_bounds__(block_of(LPR)) combine_backward_kernel(RowArgs
       w[j] = row[j] >= 0 ? g.w[pair + j0 + j] : 0.0f;
       dot[j] = 0.0f;
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
+      for (int c = 0; c < NU; ++c) {
         const int i = li + c * LPR;
-        v[j][c] = Raw8<F32>{};
-        if (g.d_w && row[j] >= 0 && i < g.chunks)
-          v[j][c] = raw8<F32>(g.rows, (int64_t)row[j] * g.chunks + i);
+        v[j][c] = {};
+        if (g.d_w && row[j] >= 0 && i < g.units)
+          v[j][c] = load_unit<U, F32, false>(g.rows, (int64_t)row[j] * g.units + i);
       }
     }
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
+    for (int c = 0; c < NU; ++c) {
       const int i = li + c * LPR;
-      float f[8];
-      values8<DF32>(dy[c], f);
+      float f[U];
+      unpack(dy[c], f);
 #pragma unroll
       for (int j = 0; j < JB; ++j) {
         if (j0 + j >= last) break;
-        float e[8];
-        values8<F32>(v[j][c], e);
+        float e[U];
+        unpack(v[j][c], e);
         float d = 0.0f;
 #pragma unroll
-        for (int x = 0; x < 8; ++x) d = fmaf(e[x], f[x], d);
-        // a row that is not there, or chunks past the row, must not meet a dy
+        for (int x = 0; x < U; ++x) d = fmaf(e[x], f[x], d);
+        // a row that is not there, or units past the row, must not meet a dy
         // that is not finite
-        if (row[j] >= 0 && i < g.chunks) {
+        if (row[j] >= 0 && i < g.units) {
           dot[j] += d;
           if (g.out_rows) {
 #pragma unroll
-            for (int x = 0; x < 8; ++x) e[x] = w[j] * f[x];
-            store8<F32>(g.out_rows, (int64_t)row[j] * g.chunks + i, e);
+            for (int x = 0; x < U; ++x) e[x] = w[j] * f[x];
+            store_unit<U, F32, false>(g.out_rows, (int64_t)row[j] * g.units + i, pack<U, F32>(e));
           }
         }
       }
@@ -230,27 +206,28 @@ __global__ void __launch_bounds__(block_of(LPR)) combine_backward_kernel(RowArgs
   }
 }
 
-// Lanes of a row of n chunks: the next power of two, up to a workgroup.
+// Lanes of a row of n units: the next power of two, up to a workgroup.
 int lanes_of(int n) { return n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : n <= 64 ? 64 : kThreads; }
 
-// Workgroups of the kernels that spread chunks over all tokens.
-unsigned chunk_groups(int chunks, int lanes, int T) {
-  return lanes == kThreads ? (unsigned)((chunks + kThreads - 1) / kThreads * T)
+// Workgroups of the kernels that spread units over all tokens.
+unsigned unit_groups(int units, int lanes, int T) {
+  return lanes == kThreads ? (unsigned)((units + kThreads - 1) / kThreads * T)
                            : (unsigned)((T + kThreads / lanes - 1) / (kThreads / lanes));
 }
 
+// NC: chunks of eight values to a lane.
 template <int LPR, int NC, bool F32, bool DF32>
 void run_backward(const RowArgs &g, hipStream_t s) {
-  constexpr int B = block_of(LPR), per = B / LPR;
+  constexpr int B = block_of(LPR), per = B / LPR, NU = NC * 8 / unit_of(F32);
   const int groups = (g.T + per - 1) / per;
   const int split = groups >= 512 ? 1 : (512 + groups - 1) / groups;
-  launch_k(COLI_K_ROWS_BACKWARD, combine_backward_kernel<LPR, NC, F32, DF32>,
+  launch_k(COLI_K_ROWS_BACKWARD, combine_backward_kernel<LPR, NU, F32, DF32>,
            dim3(groups, split < g.k ? split : g.k), dim3(B), 0, s, g);
 }
 
 template <bool F32, bool DF32>
 void pick_backward(const RowArgs &g, hipStream_t s) {
-  const int n = g.chunks;
+  const int n = g.units * unit_of(F32) / 8;
   if (n <= 8) return run_backward<8, 1, F32, DF32>(g, s);
   if (n <= 16) return run_backward<16, 1, F32, DF32>(g, s);
   if (n <= 32) return run_backward<32, 1, F32, DF32>(g, s);
@@ -270,26 +247,26 @@ int64_t row_bytes(const Layer &L, int T, int dtype) {
 
 template <bool NT>
 void pick_dispatch(const RowArgs &g, hipStream_t s) {
-  const int lanes = lanes_of(g.chunks);
+  const int lanes = lanes_of(g.units);
   launch_k(COLI_K_DISPATCH,
            lanes == 8    ? dispatch_kernel<8, NT>
            : lanes == 16 ? dispatch_kernel<16, NT>
            : lanes == 32 ? dispatch_kernel<32, NT>
            : lanes == 64 ? dispatch_kernel<64, NT>
                          : dispatch_kernel<kThreads, NT>,
-           dim3(chunk_groups(g.chunks, lanes, g.T)), dim3(kThreads), 0, s, g);
+           dim3(unit_groups(g.units, lanes, g.T)), dim3(kThreads), 0, s, g);
 }
 
 template <bool F32, bool WEIGHTED, bool NT>
 void pick_combine(const RowArgs &g, hipStream_t s) {
-  const int lanes = lanes_of(g.chunks);
+  const int lanes = lanes_of(g.units);
   launch_k(COLI_K_ROWS_COMBINE,
            lanes == 8    ? rows_combine_kernel<8, F32, WEIGHTED, NT>
            : lanes == 16 ? rows_combine_kernel<16, F32, WEIGHTED, NT>
            : lanes == 32 ? rows_combine_kernel<32, F32, WEIGHTED, NT>
            : lanes == 64 ? rows_combine_kernel<64, F32, WEIGHTED, NT>
                          : rows_combine_kernel<kThreads, F32, WEIGHTED, NT>,
-           dim3(chunk_groups(g.chunks, lanes, g.T)), dim3(kThreads), 0, s, g);
+           dim3(unit_groups(g.units, lanes, g.T)), dim3(kThreads), 0, s, g);
 }
 template <bool F32, bool WEIGHTED>
 void pick_combine(const RowArgs &g, bool nt, hipStream_t s) {
@@ -307,7 +284,7 @@ int launch_dispatch(const Layer &L, const int32_t *pos, const void *x, int dtype
   g.n_rows = n_rows;
   g.T = T;
   g.k = L.k;
-  g.chunks = L.H * (dtype == COLI_SRC_F32 ? 4 : 2) / 16;
+  g.units = L.H * (dtype == COLI_SRC_F32 ? 4 : 2) / 16;
   // Rows of twice the last cache or more are written past it: 16,384 tokens x 8
   // rows of 2048 in 105 us instead of 122, and with a reader behind 403 against
   // 396; at 384 MB the reader loses more (206 against 195 with it).
@@ -331,8 +308,8 @@ int launch_rows_combine(const Layer &L, const int32_t *pos, const float *w, cons
   g.out_f32 = y_dtype == COLI_SRC_F32;
   g.T = T;
   g.k = L.k;
-  g.chunks = L.H / 8;
   const bool f32 = rows_dtype == COLI_SRC_F32;
+  g.units = L.H / unit_of(f32);
   // Rows that fill half of the last cache or more are read past it, as they are
   // read once: 8,192 tokens x 8 rows of 6144 in 170 us instead of 183, after
   // their writer 150 instead of 197 (4,096 tokens); rows of 64 MB and less would
@@ -358,8 +335,8 @@ int launch_combine_backward(const Layer &L, const int32_t *pos, const float *w, 
   g.d_w = d_w;
   g.T = T;
   g.k = L.k;
-  g.chunks = L.H / 8;
   const bool f32 = rows_dtype == COLI_SRC_F32;
+  g.units = L.H / unit_of(f32);
   if (dy_dtype == COLI_SRC_F32)
     f32 ? pick_backward<true, true>(g, s) : pick_backward<false, true>(g, s);
   else
