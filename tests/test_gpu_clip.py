@@ -144,6 +144,18 @@ def test_repeated_captured_and_streams():
         assert np.array_equal(norm.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("out,shift", [("same", False), ("other", True), ("mixed", False),
+                                       ("mixed", True)])
+@pytest.mark.parametrize("n", [20000003, 90000001])
+def test_large(n, out, shift):
+    """Gradients of 80 and 360 MB and more, which go past the caches."""
+    sizes = [n, 5, n // 3, 100000]
+    grads, outs = _make(sizes, 0, out, shift)
+    before = [t.clone() for t in grads]
+    size = float(np.sqrt(sum(float(t.double().square().sum()) for t in before)))
+    _check(before, outs, _clip(grads, outs, 0.3 * size), 0.3 * size)
+
+
 def test_largest():
     """A gradient of over 2^31 values, in bf16, and many beside it."""
     big = torch.full(((1 << 31) + 77,), 0.5, dtype=BF, device="cuda")

@@ -197,6 +197,21 @@ def test_many_rows():
                 assert torch.equal(out["q"][at], q) and torch.equal(out["scales"][at].reshape(-1), d)
 
 
+@pytest.mark.parametrize("residual", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H", [(40001, 2048), (14001, 6144), (200001, 416)])
+def test_large_streams(T, H, residual):
+    """Calls of over 384 MB, forward, and of over 768 MB, backward."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    new = lambda dt, s: (torch.randn(T, H, generator=g, device="cuda") * s).to(dt)  # noqa: E731
+    x, res, w = new(BF, 1.0), new(TYPES[residual], 3.0), torch.rand(H, generator=g, device="cuda")
+    out = _run(x, res, w, coli.COLI_NORM_MXFP8)
+    _check(x, res, w, out)
+    q, d = _codes(out["y"], coli.COLI_NORM_MXFP8)
+    assert torch.equal(out["q"], q) and torch.equal(out["scales"].view(-1), d)
+    dy, d_total = new(BF, 1e-2), new(TYPES[residual], 1e-2)
+    _check_backward(out["total"], dy, w, d_total, _backward(out["total"], dy, w, d_total))
+
+
 # ------------------------------------------------------------------ the path
 
 @pytest.mark.parametrize("H,I,kind,act", [

@@ -241,6 +241,26 @@ def test_largest():
         assert ((d_w.view(65536, 16)[at].double() - sq).abs() <= 100 * H24 * sq).all()
 
 
+@pytest.mark.parametrize("H,dtype", [(64, F32), (128, BF), (256, BF), (256, F32), (512, BF)])
+def test_many_short_rows(H, dtype):
+    """Rows of few lanes in buffers that go past the caches, some pairs without."""
+    c = Case(65536, H, 64, 16, seed=10, drop=0.01)
+    x, rows = c.new(65536, dtype), c.new(c.n, dtype)
+    before = rows.clone()
+    coli.coli_moe_dispatch(c.L, c.r, x, 65536, rows)
+    torch.cuda.synchronize()
+    token = torch.arange(65536, device="cuda")[:, None].expand(65536, 16)
+    before[c.pos[c.has]] = x[token[c.has]]
+    assert torch.equal(rows, before)
+    rows = c.new(c.n, dtype)
+    y, dx = torch.empty(65536, H, dtype=BF, device="cuda"), torch.empty(65536, H, device="cuda")
+    coli.coli_moe_combine(c.L, c.r, rows, x, 65536, y)
+    coli.coli_moe_dispatch_backward(c.L, c.r, rows, None, 65536, dx)
+    torch.cuda.synchronize()
+    _check_sum(c, rows, c.w, x, y)
+    _check_sum(c, rows, None, None, dx)
+
+
 def test_captured():
     c = Case(300, 1024, 64, 8, seed=6)
     x, dy = c.new(300, BF), c.new(300, BF)
