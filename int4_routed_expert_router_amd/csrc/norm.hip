@@ -157,7 +157,7 @@ struct NormBackArgs {
   const void *weight;
   uint16_t *dx;
   void *d_residual;
-  float *parts;  // [gridDim.x][H] or NULL
+  float *parts;  // [gridDim.x][H] (of one workgroup: d_weight) or NULL
   int T, units;
   int weight_f32;
   float eps, inv_h;
@@ -330,10 +330,14 @@ int backward_lanes(int chunks) {
 // Workgroups, and parts of d_weight: some 768 lanes to each of the 256 CUs.
 // More would be more parts and fewer rows to each (65,536 x 2048: 768
 // workgroups 219 us, 1,024 and 1,280 226; x 1024: 1,024 141, 1,536 and 2,048
-// 113; 8,192 x 6144: 256 87, 512 89).
+// 113; 8,192 x 6144: 256 87, 512 89).  A few rows are one workgroup's work: it
+// writes d_weight itself, and the call is one launch instead of two.
 int backward_groups(int chunks, int T) {
   const int lanes = backward_lanes(chunks), block = block_of(lanes);
   const int groups = (T + block / lanes - 1) / (block / lanes);
+  // (4 rows of 6144 in 6.1 us in a row of calls instead of 8.7, alone 19.8 instead
+  // of 20.2 with the wait; 6 rows 8.1, alone 21.9; 2 rows of 16,384 7.1, 3 9.4)
+  if (groups <= (chunks <= 1024 ? 4 : 2)) return 1;
   const int most = 256 * ((768 + block - 1) / block);
   return groups < most ? groups : most;
 }
@@ -410,7 +414,8 @@ int launch_norm_backward(const coli_moe_norm_t &n, const void *total, int total_
   g.weight = n.weight;
   g.dx = dx;
   g.d_residual = d_residual;
-  g.parts = d_weight ? reinterpret_cast<float *>(ws) : nullptr;
+  const int groups = backward_groups(n.hidden / 8, T);
+  g.parts = groups == 1 || !d_weight ? d_weight : reinterpret_cast<float *>(ws);
   g.T = T;
   g.units = n.hidden / unit_of(total_dtype == COLI_SRC_F32);
   g.weight_f32 = n.weight_dtype == COLI_SRC_F32;
@@ -421,11 +426,11 @@ int launch_norm_backward(const coli_moe_norm_t &n, const void *total, int total_
   else
     pick_norm_backward<false>(g, s);
   if (hipGetLastError() != hipSuccess) return COLI_E_HIP;
-  if (!d_weight) return COLI_OK;
+  if (!d_weight || groups == 1) return COLI_OK;
   const int H = n.hidden;
   launch_k(COLI_K_NORM_REDUCE, H <= 2048 ? norm_reduce_kernel<16> : norm_reduce_kernel<64>,
            dim3(H <= 2048 ? (H + 15) / 16 : (H + 63) / 64), dim3(1024), 0, s, (const float *)ws,
-           backward_groups(H / 8, T), H, d_weight);
+           groups, H, d_weight);
   return hip_status(hipGetLastError());
 }
 

@@ -297,6 +297,16 @@ def test_norm_backward(T, H, dtype):
     _check_backward(total, dy, w, d_total, _backward(total, dy, w, d_total))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("H", [64, 128, 520, 2048, 6144, 16384])
+def test_backward_few_rows(H, dtype):
+    """On both sides of the number of rows that one workgroup takes."""
+    side = max(1, 32 * 64 // H) if H <= 512 else 1
+    for T in (2, 3, 4 * side, 4 * side + 1):
+        total, dy, w, d_total = _back_inputs(T, H, dtype, BF, True, T)
+        _check_backward(total, dy, w, d_total, _backward(total, dy, w, d_total))
+
+
 @pytest.mark.parametrize("asked", [(1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 0, 1), (0, 1, 1)])
 def test_backward_parts(asked):
     total, dy, w, d_total = _back_inputs(70, 1024, F32, BF, True, 1)
