@@ -125,7 +125,8 @@ void run_norm(const NormArgs &g, hipStream_t s) {
   const int64_t blocks = ((int64_t)g.T + RPB - 1) / RPB;
   // From half as much again as the last cache on, x, residual, total and y go
   // past it: 8,192 x 6144 in 69 us instead of 76, and 172 instead of 178 with a
-  // reader of y behind; 16,384 x 2048 (268 MB) 44 against 41.
+  // reader of y behind; fp32 16,384 x 2048 67 instead of 73, and 135 instead of
+  // 146 with the next norm behind; bf16 16,384 x 2048 (268 MB) 44 against 41.
   const int64_t bytes = (int64_t)g.T * g.units * U * (RES == 2 ? 12 : RES ? 8 : 4);
   launch_k(COLI_K_NORM,
            bytes >= int64_t(384) << 20 ? norm_kernel<LPR, NU, RES, true>
@@ -346,9 +347,10 @@ template <int LPR, int NC, bool F32>
 void run_norm_backward(const NormBackArgs &g, hipStream_t s) {
   constexpr int U = unit_of(F32), NU = NC * 8 / U;
   const int chunks = g.units * U / 8;
-  // From three times the last cache on, rows go past it: 65,536 x 2048 in 204 us
-  // instead of 213, fp32 8,192 x 8192 199 instead of 208; at 403 MB the same.
-  const bool nt = (int64_t)g.T * g.units * U * (F32 ? 16 : 8) >= int64_t(768) << 20;
+  // As in the forward pass: fp32 16,384 x 2048 (512 MB) in 95 us instead of 102,
+  // and 190 instead of 204 with the next layer's behind; 8,192 x 2048 (256 MB) 51
+  // against 49.
+  const bool nt = (int64_t)g.T * g.units * U * (F32 ? 16 : 8) >= int64_t(384) << 20;
   launch_k(COLI_K_NORM_BACKWARD,
            nt ? norm_backward_kernel<LPR, NU, F32, true> : norm_backward_kernel<LPR, NU, F32, false>,
            dim3(backward_groups(chunks, g.T)), dim3(block_of(LPR)), 0, s, g);
