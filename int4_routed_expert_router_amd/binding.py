@@ -427,10 +427,15 @@ def _shape_nk(layer: Layer, matrix: int):
     return (layer.hidden, layer.inter) if matrix == 2 else (layer.inter, layer.hidden)
 
 
+_calls = {}  # name -> function of the library
+
+
 def _run(name, on, stream, *args):
     """Calls the library on the device of tensor `on`: by default on that
     device's current stream, which is made current for the call if it is not."""
-    fn = getattr(_load(), name)
+    fn = _calls.get(name)
+    if fn is None:
+        fn = _calls[name] = getattr(_load(), name)
     dev = on.get_device()
     if dev < 0:
         raise ValueError("%s: tensors have to be on the GPU, got %s" % (name, on.device))
@@ -440,7 +445,7 @@ def _run(name, on, stream, *args):
     else:
         with torch.cuda.device(dev):
             rc = fn(*args, s)
-    if rc != COLI_OK:
+    if rc:
         raise ColiError(name, rc)
 
 
@@ -555,9 +560,10 @@ def _dtype(t, name):
     """COLI_SRC_* of a tensor (bf16 where there is none)."""
     if t is None:
         return COLI_SRC_BF16
-    if t.dtype not in _DTYPES:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
         raise ValueError("%s: expected a bfloat16 or float32 tensor, got %s" % (name, t.dtype))
-    return _DTYPES[t.dtype]
+    return code
 
 
 class Norm:
@@ -635,7 +641,7 @@ def coli_moe_forward_prefill_quantized(layer: Layer, route: Route, q, scales, T:
 
 def _route_arg(layer, route, T, dev, weights=False):
     """The route's tensors as they are now: a caller may have put others in place."""
-    c, n = route.c, T * layer.top_k
+    c, n = route.c, T * layer.c.top_k
     c.pair_pos = _arg(route.pair_pos, "route", torch.int32, n, dev)
     if weights:
         c.topk_w = _arg(route.topk_w, "route", torch.float32, n, dev)
@@ -644,20 +650,18 @@ def _route_arg(layer, route, T, dev, weights=False):
 
 def coli_moe_dispatch(layer: Layer, route: Route, x, T: int, rows, stream=None):
     """rows[pair_pos[t*k + j]] = x[t]; x and rows both bf16 or both fp32."""
-    h, dev, dt = layer.hidden, rows.get_device(), _dtype(rows, "rows")
-    _run("coli_moe_dispatch", x, stream, *_route_arg(layer, route, T, dev),
-         _arg(x, "x", rows.dtype, T * h, dev), dt, T, _arg(rows, "rows", rows.dtype, h, dev),
-         rows.numel() // h)
+    h, dev, t = layer.c.hidden, rows.get_device(), rows.dtype
+    lc, rc = _route_arg(layer, route, T, dev)
+    _run("coli_moe_dispatch", x, stream, lc, rc, _arg(x, "x", t, T * h, dev),
+         _dtype(rows, "rows"), T, _arg(rows, "rows", t, h, dev), rows.numel() // h)
 
 
 def _sum_rows(name, layer, route, rows, beside, T, out, stream):
-    h, dev = layer.hidden, rows.get_device()
-    rd, od = _dtype(rows, "rows"), _dtype(out, "y")
-    _run(name, out, stream,
-         *_route_arg(layer, route, T, dev, name == "coli_moe_combine"),
-         _arg(rows, "rows", rows.dtype, h, dev), rd, rows.numel() // h,
-         _arg(beside, "beside", rows.dtype, T * h, dev), T, _arg(out, "y", out.dtype, T * h, dev),
-         od)
+    h, dev, t = layer.c.hidden, rows.get_device(), rows.dtype
+    lc, rc = _route_arg(layer, route, T, dev, name == "coli_moe_combine")
+    _run(name, out, stream, lc, rc, _arg(rows, "rows", t, h, dev), _dtype(rows, "rows"),
+         rows.numel() // h, _arg(beside, "beside", t, T * h, dev), T,
+         _arg(out, "y", out.dtype, T * h, dev), _dtype(out, "y"))
 
 
 def coli_moe_dispatch_backward(layer: Layer, route: Route, d_rows, beside, T: int, dx,
@@ -675,7 +679,7 @@ def coli_moe_combine_backward(layer: Layer, route: Route, rows, dy, T: int, d_ro
                               stream=None):
     """d_rows (of rows' type) and d_topk_w (fp32) of coli_moe_combine; either may
     be None, and rows too without d_topk_w."""
-    h, like = layer.hidden, d_rows if rows is None else rows
+    h, like = layer.c.hidden, d_rows if rows is None else rows
     dev, rd, yd = like.get_device(), _dtype(like, "rows"), _dtype(dy, "dy")
     n = like.numel() // h
     _run("coli_moe_combine_backward", dy, stream, *_route_arg(layer, route, T, dev, True),
