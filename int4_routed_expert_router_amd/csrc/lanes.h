@@ -25,15 +25,17 @@ COLI_DEV float lanes_sum(float v) {
   return v;
 }
 
-// Sums of NV values over the LPR lanes of a row, in every one of them.  Rows
-// of more than 64 lanes take a whole workgroup, and red is its LDS for this;
-// two calls in a row need no barrier between them if they use two of them.
-template <int LPR, int NV>
-COLI_DEV void row_sums(float (&v)[NV], float (*red)[LPR > 64 ? LPR / 64 : 1]) {
+// Sums of NV values over the LPR lanes of a row, in every one of them; the
+// workgroup holds RPB rows, this lane's being the ri-th.  Rows of more than 64
+// lanes need the whole workgroup here, and red is its LDS for this; two calls in
+// a row need no barrier between them if they use two of them.
+constexpr int waves_of(int lanes) { return lanes > 64 ? lanes / 64 : 1; }
+template <int LPR, int NV, int RPB = 1>
+COLI_DEV void row_sums(float (&v)[NV], float (*red)[RPB * waves_of(LPR)], int ri = 0) {
 #pragma unroll
   for (int n = 0; n < NV; ++n) v[n] = lanes_sum<(LPR < 64 ? LPR : 64)>(v[n]);
   if (LPR <= 64) return;
-  constexpr int W = LPR > 64 ? LPR / 64 : 1;
+  constexpr int W = waves_of(LPR);
   const int wave = threadIdx.x >> 6;
   if ((threadIdx.x & 63) == 0) {
 #pragma unroll
@@ -44,7 +46,7 @@ COLI_DEV void row_sums(float (&v)[NV], float (*red)[LPR > 64 ? LPR / 64 : 1]) {
   for (int n = 0; n < NV; ++n) {
     v[n] = 0.0f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) v[n] += red[n][w];
+    for (int w = 0; w < W; ++w) v[n] += red[n][(RPB > 1 ? ri * W : 0) + w];
   }
 }
 

@@ -57,7 +57,7 @@ template <int LPR, int NU, int RES, bool NT>
 __global__ void __launch_bounds__(block_of(LPR)) norm_kernel(NormArgs g) {
   constexpr int U = unit_of(RES == 2);
   constexpr int B = block_of(LPR), RPB = B / LPR;  // rows of a workgroup
-  __shared__ float red[2][1][LPR > 64 ? LPR / 64 : 1];
+  __shared__ float red[2][1][waves_of(LPR)];
   const int li = threadIdx.x % LPR;
   int turn = 0;
   for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR; row < g.T;
@@ -158,7 +158,7 @@ struct NormBackArgs {
   const void *weight;
   uint16_t *dx;
   void *d_residual;
-  float *parts;  // [gridDim.x][H] (of one workgroup: d_weight) or NULL
+  float *parts;  // of d_weight [gridDim.x][H] (one workgroup: d_weight itself), or NULL
   int T, units;
   int weight_f32;
   float eps, inv_h;
@@ -192,11 +192,10 @@ COLI_DEV void load_row(const NormBackArgs &g, int64_t row, int li, BackRow<NU, F
 // n s, come from the one pass that loads the row.  A workgroup goes over rows
 // with the next one's loads in flight (up to 8192 values), and keeps its part
 // of d_weight in registers.
-template <int LPR, int NU, bool F32, bool NT>
-__global__ void __launch_bounds__(block_of(LPR)) norm_backward_kernel(NormBackArgs g) {
-  constexpr int U = unit_of(F32);
-  constexpr int B = block_of(LPR), RPB = B / LPR;  // rows of a workgroup
-  __shared__ float red[2][2][LPR > 64 ? LPR / 64 : 1];
+template <int LPR, int NU, bool F32, bool NT, int B>
+__global__ void __launch_bounds__(B) norm_backward_kernel(NormBackArgs g) {
+  constexpr int U = unit_of(F32), RPB = B / LPR;  // rows of a workgroup
+  __shared__ float red[2][2][(LPR > 64 ? RPB : 1) * waves_of(LPR)];
   const int li = threadIdx.x % LPR, ri = threadIdx.x / LPR;
   float dw[NU][U];
 #pragma unroll
@@ -204,14 +203,15 @@ __global__ void __launch_bounds__(block_of(LPR)) norm_backward_kernel(NormBackAr
 #pragma unroll
     for (int j = 0; j < U; ++j) dw[c][j] = 0.0f;
   const int64_t step = (int64_t)gridDim.x * RPB;
-  int64_t row = (int64_t)blockIdx.x * RPB + ri;
+  int64_t first = (int64_t)blockIdx.x * RPB;  // the same for the whole workgroup
   // two chunks to a lane leave no registers for a second row (fp32 4,096 x 16,384:
   // 218 us, with it 272)
   constexpr bool kAhead = NU * U == 8;
   BackRow<NU, F32> a, next;
-  if (kAhead) load_row<LPR, NU, F32, NT>(g, row, li, a);
+  if (kAhead) load_row<LPR, NU, F32, NT>(g, first + ri, li, a);
   int turn = 0;
-  for (; row < g.T; row += step, turn ^= 1) {
+  for (; first < g.T; first += step, turn ^= 1) {
+    const int64_t row = first + ri;  // past the last: zeros, and no results
     if (kAhead)
       load_row<LPR, NU, F32, NT>(g, row + step, li, next);
     else
@@ -230,14 +230,14 @@ __global__ void __launch_bounds__(block_of(LPR)) norm_backward_kernel(NormBackAr
         sum[1] = fmaf(dy[j] * w[j], v[j], sum[1]);
       }
     }
-    row_sums<LPR, 2>(sum, red[turn]);
+    row_sums<LPR, 2, (LPR > 64 ? RPB : 1)>(sum, red[turn], ri);
     const float r = rsqrtf(fmaf(sum[0], g.inv_h, g.eps));
     const float m = sum[1] * g.inv_h * r;  // mean(n h)
     const int64_t base = row * g.units;
 #pragma unroll
     for (int c = 0; c < NU; ++c) {
       const int i = li + c * LPR;
-      if (i >= g.units) continue;
+      if (i >= g.units || (RPB > 1 && row >= g.T)) continue;
       float v[U], dy[U], o[U], w[U], d[U];
       unpack(a.s[c], v);
       unpack(a.o[c], o);
@@ -331,29 +331,43 @@ int backward_lanes(int chunks) {
 // Workgroups, and parts of d_weight: some 768 lanes to each of the 256 CUs.
 // More would be more parts and fewer rows to each (65,536 x 2048: 768
 // workgroups 219 us, 1,024 and 1,280 226; x 1024: 1,024 141, 1,536 and 2,048
-// 113; 8,192 x 6144: 256 87, 512 89).  A few rows are one workgroup's work: it
-// writes d_weight itself, and the call is one launch instead of two.
+// 113; 8,192 x 6144: 256 87, 512 89).
 int backward_groups(int chunks, int T) {
   const int lanes = backward_lanes(chunks), block = block_of(lanes);
   const int groups = (T + block / lanes - 1) / (block / lanes);
-  // (4 rows of 6144 in 6.1 us in a row of calls instead of 8.7, alone 19.8 instead
-  // of 20.2 with the wait; 6 rows 8.1, alone 21.9; 2 rows of 16,384 7.1, 3 9.4)
-  if (groups <= (chunks <= 1024 ? 4 : 2)) return 1;
   const int most = 256 * ((768 + block - 1) / block);
   return groups < most ? groups : most;
 }
 
+// Whether one workgroup of few_of threads takes all rows where d_weight is asked
+// for: it writes that itself, and the call is one launch instead of two.  Up to
+// four turns of its rows: in a row of calls 16 rows of 2048 in 6.9 us instead of
+// 8.6, alone 20.1 against 19.4 with the wait, 12 rows 18.9 against 19.4; two of
+// 16,384 7.1, three 9.4.
+constexpr int few_of(int lanes) { return lanes == 768 ? 768 : 1024; }
+bool few_rows(int chunks, int T) {
+  const int lanes = backward_lanes(chunks);
+  return T <= (chunks <= 1024 ? 4 : 2) * (few_of(lanes) / lanes);
+}
+
+// NC: chunks of eight values to a lane.
 template <int LPR, int NC, bool F32>
 void run_norm_backward(const NormBackArgs &g, hipStream_t s) {
-  constexpr int U = unit_of(F32), NU = NC * 8 / U;
+  constexpr int U = unit_of(F32), NU = NC * 8 / U, B = block_of(LPR), FEW = few_of(LPR);
   const int chunks = g.units * U / 8;
+  if (g.parts && few_rows(chunks, g.T)) {
+    launch_k(COLI_K_NORM_BACKWARD, norm_backward_kernel<LPR, NU, F32, false, FEW>, dim3(1),
+             dim3(FEW), 0, s, g);
+    return;
+  }
   // As in the forward pass: fp32 16,384 x 2048 (512 MB) in 95 us instead of 102,
   // and 190 instead of 204 with the next layer's behind; 8,192 x 2048 (256 MB) 51
   // against 49.
   const bool nt = (int64_t)g.T * g.units * U * (F32 ? 16 : 8) >= int64_t(384) << 20;
   launch_k(COLI_K_NORM_BACKWARD,
-           nt ? norm_backward_kernel<LPR, NU, F32, true> : norm_backward_kernel<LPR, NU, F32, false>,
-           dim3(backward_groups(chunks, g.T)), dim3(block_of(LPR)), 0, s, g);
+           nt ? norm_backward_kernel<LPR, NU, F32, true, B>
+              : norm_backward_kernel<LPR, NU, F32, false, B>,
+           dim3(backward_groups(chunks, g.T)), dim3(B), 0, s, g);
 }
 
 template <bool F32>
@@ -416,8 +430,8 @@ int launch_norm_backward(const coli_moe_norm_t &n, const void *total, int total_
   g.weight = n.weight;
   g.dx = dx;
   g.d_residual = d_residual;
-  const int groups = backward_groups(n.hidden / 8, T);
-  g.parts = groups == 1 || !d_weight ? d_weight : reinterpret_cast<float *>(ws);
+  const bool few = few_rows(n.hidden / 8, T);
+  g.parts = few || !d_weight ? d_weight : reinterpret_cast<float *>(ws);
   g.T = T;
   g.units = n.hidden / unit_of(total_dtype == COLI_SRC_F32);
   g.weight_f32 = n.weight_dtype == COLI_SRC_F32;
@@ -428,11 +442,11 @@ int launch_norm_backward(const coli_moe_norm_t &n, const void *total, int total_
   else
     pick_norm_backward<false>(g, s);
   if (hipGetLastError() != hipSuccess) return COLI_E_HIP;
-  if (!d_weight || groups == 1) return COLI_OK;
+  if (!d_weight || few) return COLI_OK;
   const int H = n.hidden;
   launch_k(COLI_K_NORM_REDUCE, H <= 2048 ? norm_reduce_kernel<16> : norm_reduce_kernel<64>,
            dim3(H <= 2048 ? (H + 15) / 16 : (H + 63) / 64), dim3(1024), 0, s, (const float *)ws,
-           groups, H, d_weight);
+           backward_groups(H / 8, T), H, d_weight);
   return hip_status(hipGetLastError());
 }
 

@@ -8,8 +8,9 @@ REL = 64 half steps on y before its rounding to bf16, 2^-8.  Gradients are sums
 of products: 128 half steps of the sum of the absolute values of their terms,
 mean(n h) with that of |n h|.  d_weight adds rows one after another, spread over
 256 groups or more (T / 256 + 1 additions), up to 32 of them side by side, and
-up to 1,536 groups, every 64th one after another (24) and then 64 sums: DW = 193
-half steps beside T / 256, of which 64 are those of each h."""
+up to 1,536 groups, every 64th one after another (24) and then 64 sums; or, for
+a few rows, four and up to 128 side by side.  DW = 193 half steps beside T /
+256, of which 64 are those of each h, is over both."""
 import numpy as np
 import pytest
 import torch
@@ -298,11 +299,11 @@ def test_norm_backward(T, H, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("H", [64, 128, 520, 2048, 6144, 16384])
-def test_backward_few_rows(H, dtype):
+@pytest.mark.parametrize("H,few", [(64, 512), (128, 256), (256, 128), (512, 64), (520, 32),
+                                   (2048, 16), (4096, 8), (6144, 4), (8192, 4), (16384, 2)])
+def test_backward_few_rows(H, few, dtype):
     """On both sides of the number of rows that one workgroup takes."""
-    side = max(1, 32 * 64 // H) if H <= 512 else 1
-    for T in (2, 3, 4 * side, 4 * side + 1):
+    for T in (2, 3, few - 1, few, few + 1):
         total, dy, w, d_total = _back_inputs(T, H, dtype, BF, True, T)
         _check_backward(total, dy, w, d_total, _backward(total, dy, w, d_total))
 
