@@ -6,8 +6,8 @@
 //
 // Memory bounds both: a row stays in registers between its sum and its
 // results, so everything moves once.  16,384 x 6144 with MXFP8 codes (909 MB):
-// 158 us, 5.8 TB/s (a copy of 1 GiB on this card: 5.1); the gradients at 8,192
-// with an fp32 stream (805 MB): 150 us.  A row lies over as many lanes as keep a
+// 157 to 161 us, 5.7 TB/s (a copy of 1 GiB on this card: 5.1); the gradients at
+// 8,192 with an fp32 stream (805 MB): 150 us.  A row lies over as many lanes as keep a
 // lane's share at one chunk of eight values (forward: up to four, with more
 // rows at work instead); up to 64 lanes several rows share a workgroup and sum
 // without LDS.
