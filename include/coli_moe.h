@@ -627,8 +627,9 @@ int coli_moe_forward_prefill_quantized(const coli_moe_layer_t *layer,
  * offsets[e] .. offsets[e+1]).  A caller may write others: a pair whose
  * pair_pos is outside [0, n_rows) has no row (it went over an expert's limit,
  * or its expert is on another device); the rows of different pairs have to be
- * different.  Rows that no pair owns are not written, and what they hold does
- * not matter.
+ * different.  Such a route is for these calls alone: the forward calls need
+ * the positions of coli_moe_route.  Rows that no pair owns are not written, and
+ * what they hold does not matter.
  * These calls read route->pair_pos and, where stated, route->topk_w, and H, E
  * and k of `layer` (no weights).  T in [1, 65536], T*k <= 2^20, n_rows in
  * [1, 2^21].  Element types are COLI_SRC_BF16 or COLI_SRC_F32; sums are fp32,

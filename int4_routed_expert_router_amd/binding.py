@@ -234,6 +234,9 @@ class Route:
         self.union_ids = torch.empty(E, **i32)
         self.n_union = torch.empty(1, **i32)
         self.c = _RouteC(*[_ptr(getattr(self, n)) for n, _ in _RouteC._fields_])
+        # for the calls on rows by expert, which take positions and weights that
+        # a caller may have replaced
+        self.rows_c = _RouteC.from_buffer_copy(self.c)
 
 
 def _need(t, name, dtype, numel, dev):
@@ -640,8 +643,8 @@ def coli_moe_forward_prefill_quantized(layer: Layer, route: Route, q, scales, T:
 
 
 def _route_arg(layer, route, T, dev, weights=False):
-    """The route's tensors as they are now: a caller may have put others in place."""
-    c, n = route.c, T * layer.c.top_k
+    """The route's positions and weights as they are now."""
+    c, n = route.rows_c, T * layer.c.top_k
     c.pair_pos = _arg(route.pair_pos, "route", torch.int32, n, dev)
     if weights:
         c.topk_w = _arg(route.topk_w, "route", torch.float32, n, dev)

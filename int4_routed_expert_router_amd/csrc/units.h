@@ -6,9 +6,8 @@
 
 namespace coli {
 
-// Loads and stores that leave the caches to others (NT), for buffers that are
-// several times the 256 MB of the chip's last cache: their own next reader
-// finds nothing of them there anyway.
+// Loads and stores that leave the caches to others (NT), for buffers that take
+// up much of the 256 MB of the chip's last cache.
 typedef unsigned int coli_u32x4 __attribute__((ext_vector_type(4)));
 template <bool NT>
 COLI_DEV uint4 load16(const uint4 *p) {

@@ -174,8 +174,10 @@ def test_gradients_are_those_of_the_forward_calls():
 
 
 def test_a_route_of_other_tensors():
-    """Positions and weights that the caller put in place of the route's own."""
+    """Positions and weights that the caller put in place of the route's own;
+    what the forward calls read stays the route's."""
     c = Case(20, 256, 8, 2, seed=9)
+    own = c.r.pair_pos, c.r.topk_w
     x, y = c.new(20, F32), torch.empty(20, 256, device="cuda")
     c.r.pair_pos = torch.randperm(40, generator=c.g, device="cuda").to(torch.int32)
     c.r.topk_w = torch.rand(40, generator=c.g, device="cuda")
@@ -187,6 +189,7 @@ def test_a_route_of_other_tensors():
     torch.cuda.synchronize()
     assert torch.equal(rows[c.pos], x[:, None, :].expand(20, 2, 256))
     _check_sum(c, rows, c.w, None, y)
+    assert (c.r.c.pair_pos, c.r.c.topk_w) == tuple(t.data_ptr() for t in own)
 
 
 def test_with_nothing_but_missing_pairs():
