@@ -742,7 +742,7 @@ enum {
   COLI_K_PROJECT_REDUCE = 25, COLI_K_PROJECT_STREAM = 26, COLI_K_PROJECT_COMBINE = 27,
   COLI_K_NORM = 28, COLI_K_NORM_BACKWARD = 29, COLI_K_NORM_REDUCE = 30, COLI_K_DISPATCH = 31,
   COLI_K_ROWS_COMBINE = 32, COLI_K_ROWS_BACKWARD = 33, COLI_K_CLIP_NORM = 34,
-  COLI_K_CLIP_SCALE = 35, COLI_K_COUNT = 36
+  COLI_K_CLIP_SCALE = 35, COLI_K_CLIP_FINISH = 36, COLI_K_COUNT = 37
 };
 typedef struct coli_moe_trace {
   void **start;     /* hipEvent_t[capacity] */

@@ -50,7 +50,7 @@ KERNEL_NAMES = ["route_fused", "route_topk", "route_group", "decode_gateup", "de
                 "project_shrink", "project_gemm", "project_finish", "project_grads",
                 "project_reduce", "project_stream", "project_combine", "norm", "norm_backward",
                 "norm_reduce", "dispatch", "rows_combine", "rows_backward", "clip_norm",
-                "clip_scale"]
+                "clip_scale", "clip_finish"]
 
 
 class _RouteC(ctypes.Structure):

@@ -1,10 +1,12 @@
 // clip.hip -- the norm over many gradients, and clipping.
 //
 // A plan cuts the gradients into items of a few thousand values on the host,
-// so that one launch goes over any number of tensors of any sizes.  The first
-// kernel adds up squares, a partial sum to a workgroup; every workgroup of the
-// second adds the partial sums up again, in the same order, and scales its
-// items.  A few items are one workgroup's work, and one launch.
+// so that one launch goes over any number of tensors of any sizes.  One kernel
+// adds up squares, a partial sum to a workgroup, and another scales: up to 128 MB
+// its workgroups add the partial sums up themselves, in the same order, beyond
+// that a small kernel in between does.  A few items are one workgroup's work, and
+// one launch.  Memory bounds large ones: 656 MB in 305 to 317 us, read at 6.8 TB/s
+// for the sum, then read and written at 6.0.
 #include <math.h>
 
 #include <algorithm>
@@ -115,11 +117,10 @@ COLI_DEV void item_scale(const void *g, void *o, int n, float f, int tid) {
 #pragma unroll
       for (int j = 0; j < V; j += 4)
         store16<NT && F32>(reinterpret_cast<uint4 *>(oat) + (V * i + j) / 4,
-                    make_uint4(__float_as_uint(v[j]), __float_as_uint(v[j + 1]),
-                               __float_as_uint(v[j + 2]), __float_as_uint(v[j + 3])));
+                           make_uint4(__float_as_uint(v[j]), __float_as_uint(v[j + 1]),
+                                      __float_as_uint(v[j + 2]), __float_as_uint(v[j + 3])));
     } else if (F32) {
-      reinterpret_cast<uint2 *>(oat)[i] =
-          make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+      reinterpret_cast<uint2 *>(oat)[i] = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
     } else {
       float w[8];
 #pragma unroll
@@ -202,8 +203,7 @@ __global__ void __launch_bounds__(kThreads) clip_norm_kernel(
 }
 
 // One item to a workgroup: with the norm's grid, several to each, 656 MB take
-// 254 us instead of 222.
-template <bool NT>
+// 254 us instead of 222.  Every workgroup adds the partial sums up itself.
 __global__ void __launch_bounds__(kThreads) clip_scale_kernel(
     const coli_moe_clip_item_t *__restrict__ items, const double *__restrict__ parts, int n_parts,
     float max_norm, float *__restrict__ norm) {
@@ -211,7 +211,24 @@ __global__ void __launch_bounds__(kThreads) clip_scale_kernel(
   double a = 0.0;
   for (int i = threadIdx.x; i < n_parts; i += kThreads) a += parts[i];
   const float f = factor(group_sum64<kThreads>(a, red), max_norm, norm);
-  scale<kThreads, NT>(items[blockIdx.x], f, threadIdx.x);
+  scale<kThreads, false>(items[blockIdx.x], f, threadIdx.x);
+}
+
+// For many items that sum is a launch of its own, of one workgroup ...
+__global__ void __launch_bounds__(kThreads) clip_finish_kernel(const double *__restrict__ parts,
+                                                               int n_parts, float max_norm,
+                                                               float *__restrict__ norm) {
+  __shared__ double red[kThreads / 64];
+  double a = 0.0;
+  for (int i = threadIdx.x; i < n_parts; i += kThreads) a += parts[i];
+  factor(group_sum64<kThreads>(a, red), max_norm, norm);
+}
+
+// ... whose factor is all that the others read.
+template <bool NT>
+__global__ void __launch_bounds__(kThreads) clip_scale_many_kernel(
+    const coli_moe_clip_item_t *__restrict__ items, const float *__restrict__ norm) {
+  scale<kThreads, NT>(items[blockIdx.x], norm[1], threadIdx.x);
 }
 
 // Both in one workgroup, for a few items: a wave to an item.  16 items take 6.8 us
@@ -346,21 +363,31 @@ int launch_clip(const coli_moe_clip_item_t *items, int64_t n_items, float max_no
   const int64_t rounds = (n_items + kGroups - 1) / kGroups;
   const int grid = (int)((n_items + rounds - 1) / rounds);
   // From a quarter of the chip's last cache on the sum reads past it: 656 MB in
-  // 95 us instead of 141, 110 MB in 18 instead of 29.  Below, the second kernel
-  // gains more by finding there what the first has read (18 MB: 13.2 us for
-  // both, 14.1 past it; 66 MB: 39 either way).  The second kernel reads and
-  // writes past it where the results would not stay there anyway (656 MB: 222 us
-  // instead of 233; all of 256 MB 127 instead of 141, and 267 instead of 276 with
-  // an update from them behind; 128 MB 65 against 62).
+  // 95 us instead of 141, 110 MB in 18 instead of 29.  Below, what writes the
+  // results gains more by finding there what the sum has read (18 MB: 13.2 us for
+  // both, 14.1 past it; 66 MB: 39 either way).
   const int64_t most = n_items * kItem * 4;  // bytes, if fp32
   launch_k(COLI_K_CLIP_NORM,
            most >= int64_t(64) << 20 ? clip_norm_kernel<true> : clip_norm_kernel<false>,
            dim3(grid), dim3(kThreads), 0, s, items, n_items, parts);
   if (hipGetLastError() != hipSuccess) return COLI_E_HIP;
+  // From 128 MB on the partial sums are added up once: gradients in place that
+  // need no clipping take 109 us instead of 121 for 656 MB, 26 instead of 27 for
+  // 128 MB (16 MB: 11.5 against 9.2); clipped ones the same either way.
+  if (most < int64_t(128) << 20) {
+    launch_k(COLI_K_CLIP_SCALE, clip_scale_kernel, dim3((unsigned)n_items), dim3(kThreads), 0, s,
+             items, (const double *)parts, grid, max_norm, norm);
+    return hip_status(hipGetLastError());
+  }
+  launch_k(COLI_K_CLIP_FINISH, clip_finish_kernel, dim3(1), dim3(kThreads), 0, s,
+           (const double *)parts, grid, max_norm, norm);
+  if (hipGetLastError() != hipSuccess) return COLI_E_HIP;
+  // Results that would not stay in the last cache anyway are read and written
+  // past it (656 MB: 222 us instead of 233; all of 256 MB 127 instead of 141, and
+  // 267 instead of 276 with an update from them behind; 128 MB 65 against 62).
   launch_k(COLI_K_CLIP_SCALE,
-           most >= int64_t(256) << 20 ? clip_scale_kernel<true> : clip_scale_kernel<false>,
-           dim3((unsigned)n_items), dim3(kThreads), 0, s, items, (const double *)parts, grid,
-           max_norm, norm);
+           most >= int64_t(256) << 20 ? clip_scale_many_kernel<true> : clip_scale_many_kernel<false>,
+           dim3((unsigned)n_items), dim3(kThreads), 0, s, items, (const float *)norm);
   return hip_status(hipGetLastError());
 }
 

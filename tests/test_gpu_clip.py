@@ -153,6 +153,7 @@ def test_large(n, out, shift):
     grads, outs = _make(sizes, 0, out, shift)
     before = [t.clone() for t in grads]
     size = float(np.sqrt(sum(float(t.double().square().sum()) for t in before)))
+    _check(before, outs, _clip(grads, outs, 1.5 * size), 1.5 * size)  # nothing to clip
     _check(before, outs, _clip(grads, outs, 0.3 * size), 0.3 * size)
 
 
