@@ -219,7 +219,12 @@ class Layer:
 
 
 class Route:
-    """Device buffers written by coli_moe_route for up to `max_tokens` tokens."""
+    """Device buffers written by coli_moe_route for up to `max_tokens` tokens.
+
+    A caller may put other tensors in place of `pair_pos` and `topk_w`, for the
+    calls on rows by expert alone: the forward calls keep reading what
+    coli_moe_route wrote, and the next coli_moe_route[_hidden] puts its own
+    tensors back."""
 
     def __init__(self, layer: Layer, max_tokens: int, device="cuda"):
         P = max_tokens * layer.top_k
@@ -234,9 +239,16 @@ class Route:
         self.union_ids = torch.empty(E, **i32)
         self.n_union = torch.empty(1, **i32)
         self.c = _RouteC(*[_ptr(getattr(self, n)) for n, _ in _RouteC._fields_])
+        # what self.c points at stays alive, whatever becomes of the attributes
+        self._own = {n: getattr(self, n) for n, _ in _RouteC._fields_}
+        self._kept = [t.detach() for t in self._own.values()]
         # for the calls on rows by expert, which take positions and weights that
         # a caller may have replaced
         self.rows_c = _RouteC.from_buffer_copy(self.c)
+
+    def _routed(self):
+        """The attributes name what a route call wrote."""
+        vars(self).update(self._own)
 
 
 def _need(t, name, dtype, numel, dev):
@@ -338,6 +350,7 @@ def coli_moe_route(layer: Layer, logits, sel_bias, T: int, route: Route, ws=None
     _check("coli_moe_route", _load().coli_moe_route(
         ctypes.byref(layer.c), _ptr(logits), _ptr(sel_bias), T, ctypes.byref(route.c),
         _ptr(ws), nb, _stream(stream)))
+    route._routed()
 
 
 def coli_moe_route_hidden(layer: Layer, w_router, x, sel_bias, T: int, logits, route: Route,
@@ -346,6 +359,7 @@ def coli_moe_route_hidden(layer: Layer, w_router, x, sel_bias, T: int, logits, r
     _check("coli_moe_route_hidden", _load().coli_moe_route_hidden(
         ctypes.byref(layer.c), _ptr(w_router), _ptr(x), _ptr(sel_bias), T, _ptr(logits),
         ctypes.byref(route.c), _ptr(ws), nb, _stream(stream)))
+    route._routed()
 
 
 def coli_moe_forward_decode(layer: Layer, route: Route, x, T: int, y, y_dtype: int, ws,
@@ -632,7 +646,7 @@ def coli_moe_forward_prefill_quantized(layer: Layer, route: Route, q, scales, T:
     """coli_moe_forward_prefill of the codes that coli_moe_norm writes."""
     dev, n = q.get_device(), T * layer.hidden
     qt, st = _CODES[COLI_NORM_MXFP8 if layer.c.flags & COLI_ACT_MXFP8 else COLI_NORM_Q8_0]
-    _need(route.topk_w, "route", torch.float32, T * layer.top_k, dev)
+    _need(route._own["topk_w"], "route", torch.float32, T * layer.top_k, dev)
     for w in (layer.q4, layer.scales):
         if isinstance(w, torch.Tensor) and w.get_device() != dev:
             raise ValueError("the layer's weights on %s, q on %s" % (w.device, q.device))
