@@ -585,14 +585,16 @@ def _dtype(t, name):
 
 class Norm:
     """A root-mean-square norm over `hidden` values: weight [hidden] bf16 or
-    fp32 on the device (None: ones)."""
+    fp32 on the device (None: ones).  The calls take the weight as it is then."""
 
     def __init__(self, hidden: int, weight=None, eps: float = 1e-6):
         if weight is not None:
             _dtype(weight, "weight")
             _need(weight, "weight", weight.dtype, hidden, weight.get_device())
-        self.weight, self.hidden = weight, hidden  # keep the tensor alive
+        self.weight, self.seen = weight, weight  # seen: the tensor that c describes
         self.c = _NormC(hidden, eps, _ptr(weight), _dtype(weight, "weight"))
+
+    hidden = property(lambda s: s.c.hidden)
 
 
 def coli_moe_norm_workspace_bytes(norm: Norm, T: int) -> int:
@@ -605,10 +607,16 @@ def norm_workspace(norm: Norm, T: int, device="cuda") -> torch.Tensor:
                        device=device if norm.weight is None else norm.weight.device)
 
 
-def _norm_weight(norm, dev, x):
-    if norm.weight is not None and norm.weight.get_device() != dev:
-        raise ValueError("the norm's weight on %s, its input on %s"
-                         % (norm.weight.device, x.device))
+def _norm_arg(norm, dev, x):
+    """The norm's width, and its description with the weight as it is now."""
+    w, c = norm.weight, norm.c
+    if w is not None and w.get_device() != dev:
+        raise ValueError("the norm's weight on %s, its input on %s" % (w.device, x.device))
+    if w is not norm.seen or (w is not None and w.data_ptr() != c.weight):
+        dtype = _dtype(w, "weight")
+        c.weight = None if w is None else _arg(w, "weight", w.dtype, c.hidden, dev)
+        c.weight_dtype, norm.seen = dtype, w
+    return c.hidden, ctypes.byref(c)
 
 
 def coli_moe_norm(norm: Norm, x, residual, total, T: int, y, fmt: int = COLI_NORM_PLAIN, q=None,
@@ -616,11 +624,12 @@ def coli_moe_norm(norm: Norm, x, residual, total, T: int, y, fmt: int = COLI_NOR
     """total = residual + x; y (bf16) and the codes q, scales of its norm (see
     include/coli_moe.h).  residual and total, y, or q and scales may be None;
     q int8 and scales fp16 for Q8_0, both uint8 for MXFP8."""
-    n, dev = T * norm.hidden, x.get_device()
-    _norm_weight(norm, dev, x)
+    dev = x.get_device()
+    h, c = _norm_arg(norm, dev, x)
+    n = T * h
     rd, stype = _dtype(residual, "residual"), None if residual is None else residual.dtype
     qt, st = _CODES.get(fmt, (None, None))
-    _run("coli_moe_norm", x, stream, ctypes.byref(norm.c), _arg(x, "x", torch.bfloat16, n, dev),
+    _run("coli_moe_norm", x, stream, c, _arg(x, "x", torch.bfloat16, n, dev),
          _arg(residual, "residual", stype, n, dev), rd, T, _arg(total, "total", stype, n, dev),
          _arg(y, "y", torch.bfloat16, n, dev), fmt, _arg(q, "q", qt, n, dev),
          _arg(scales, "scales", st, n // 32, dev))
@@ -631,13 +640,14 @@ def coli_moe_norm_backward(norm: Norm, total, T: int, dy, d_total, dx, d_residua
     """dx (bf16), d_residual (total's type) and d_weight (fp32) of coli_moe_norm
     from total (x where there was no residual); d_total and any of the outputs
     may be None, ws too without d_weight."""
-    n, dev, td, stype = T * norm.hidden, total.get_device(), _dtype(total, "total"), total.dtype
-    _norm_weight(norm, dev, total)
-    _run("coli_moe_norm_backward", total, stream, ctypes.byref(norm.c),
+    dev, td, stype = total.get_device(), _dtype(total, "total"), total.dtype
+    h, c = _norm_arg(norm, dev, total)
+    n = T * h
+    _run("coli_moe_norm_backward", total, stream, c,
          _arg(total, "total", stype, n, dev), td, _arg(dy, "dy", torch.bfloat16, n, dev),
          _arg(d_total, "d_total", stype, n, dev), T, _arg(dx, "dx", torch.bfloat16, n, dev),
          _arg(d_residual, "d_residual", stype, n, dev),
-         _arg(d_weight, "d_weight", torch.float32, norm.hidden, dev),
+         _arg(d_weight, "d_weight", torch.float32, h, dev),
          *((None, 0) if ws is None else _ws(ws, total)))
 
 
