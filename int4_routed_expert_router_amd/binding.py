@@ -717,13 +717,20 @@ def coli_moe_combine_backward(layer: Layer, route: Route, rows, dy, T: int, d_ro
 
 class Gradients:
     """A plan for clipping `grads` (bf16 or fp32 tensors on one device), in place
-    or into `out` (as many tensors of the same sizes, of either type)."""
+    or into `out` (as many tensors of the same sizes, of either type).
+
+    It is made on the host and is one of addresses: it serves any number of
+    calls as long as the tensors stay where they are, and where one moves
+    another plan has to be made.  The memory itself it keeps alive."""
 
     def __init__(self, grads, out=None):
         self.grads = list(grads)
         self.out = self.grads if out is None else list(out)
         if not self.grads or len(self.out) != len(self.grads):
             raise ValueError("%d gradients and %d outputs" % (len(self.grads), len(self.out)))
+        self._kept = [t.detach() for t in self.grads]
+        if out is not None:
+            self._kept += [t.detach() for t in self.out]
         dev = self.grads[0].get_device()
         c = (_GradientC * len(self.grads))()
         for i, (g, o) in enumerate(zip(self.grads, self.out)):
