@@ -2,15 +2,16 @@
 //
 // A plan cuts the gradients into items of a few thousand values on the host,
 // so that one launch goes over any number of tensors of any sizes.  One kernel
-// adds up squares, a partial sum to a workgroup, and another scales: up to 128 MB
-// its workgroups add the partial sums up themselves, in the same order, beyond
-// that a small kernel in between does.  A few items are one workgroup's work, and
-// one launch.  Memory bounds large ones: 656 MB in 305 to 317 us, read at 6.8 TB/s
-// for the sum, then read and written at 6.0.
+// adds up squares, a partial sum to a workgroup, and another scales: up to some
+// thousand items its workgroups add the partial sums up themselves, in the same
+// order, beyond that a small kernel in between does.  A few items are one
+// workgroup's work, and one launch.  Memory bounds large ones: 656 MB in 305 to
+// 326 us, read at 6.8 TB/s for the sum, then read and written at 6.0.
 #include <math.h>
 
 #include <algorithm>
 
+#include "clip_rules.h"
 #include "internal.h"
 #include "units.h"
 
@@ -155,6 +156,11 @@ COLI_DEV double squares_of(const coli_moe_clip_item_t &it, int tid) {
                               : item_squares<false, THREADS, NT>(it.grad, it.n, tid);
 }
 
+// Whether an item's grad is of that many bytes or more.
+COLI_DEV bool from_bytes(const coli_moe_clip_item_t &it, int from) {
+  return clip_item_bytes(it.n, it.dtypes & kGradF32) >= from;
+}
+
 template <int THREADS, bool NT>
 COLI_DEV void scale(const coli_moe_clip_item_t &it, float f, int tid) {
   if (it.out == it.grad && f == 1.0f) return;
@@ -191,13 +197,16 @@ COLI_DEV float factor(double squares, float max_norm, float *norm) {
   return f;
 }
 
-template <bool NT>
 __global__ void __launch_bounds__(kThreads) clip_norm_kernel(
-    const coli_moe_clip_item_t *__restrict__ items, int64_t n_items, double *__restrict__ parts) {
+    const coli_moe_clip_item_t *__restrict__ items, int64_t n_items, int past_from,
+    double *__restrict__ parts) {
   __shared__ double red[kThreads / 64];
   double a = 0.0;
-  for (int64_t i = blockIdx.x; i < n_items; i += gridDim.x)
-    a += squares_of<kThreads, NT>(items[i], threadIdx.x);
+  for (int64_t i = blockIdx.x; i < n_items; i += gridDim.x) {
+    const coli_moe_clip_item_t it = items[i];
+    a += from_bytes(it, past_from) ? squares_of<kThreads, true>(it, threadIdx.x)
+                                   : squares_of<kThreads, false>(it, threadIdx.x);
+  }
   a = group_sum64<kThreads>(a, red);
   if (threadIdx.x == 0) parts[blockIdx.x] = a;
 }
@@ -225,10 +234,14 @@ __global__ void __launch_bounds__(kThreads) clip_finish_kernel(const double *__r
 }
 
 // ... whose factor is all that the others read.
-template <bool NT>
 __global__ void __launch_bounds__(kThreads) clip_scale_many_kernel(
-    const coli_moe_clip_item_t *__restrict__ items, const float *__restrict__ norm) {
-  scale<kThreads, NT>(items[blockIdx.x], norm[1], threadIdx.x);
+    const coli_moe_clip_item_t *__restrict__ items, int past_from, const float *__restrict__ norm) {
+  const coli_moe_clip_item_t it = items[blockIdx.x];
+  const float f = norm[1];
+  if (from_bytes(it, past_from))
+    scale<kThreads, true>(it, f, threadIdx.x);
+  else
+    scale<kThreads, false>(it, f, threadIdx.x);
 }
 
 // Both in one workgroup, for a few items: a wave to an item.  16 items take 6.8 us
@@ -362,19 +375,10 @@ int launch_clip(const coli_moe_clip_item_t *items, int64_t n_items, float max_no
   // every workgroup the same number of items, up to one
   const int64_t rounds = (n_items + kGroups - 1) / kGroups;
   const int grid = (int)((n_items + rounds - 1) / rounds);
-  // From a quarter of the chip's last cache on the sum reads past it: 656 MB in
-  // 95 us instead of 141, 110 MB in 18 instead of 29.  Below, what writes the
-  // results gains more by finding there what the sum has read (18 MB: 13.2 us for
-  // both, 14.1 past it; 66 MB: 39 either way).
-  const int64_t most = n_items * kItem * 4;  // bytes, if fp32
-  launch_k(COLI_K_CLIP_NORM,
-           most >= int64_t(64) << 20 ? clip_norm_kernel<true> : clip_norm_kernel<false>,
-           dim3(grid), dim3(kThreads), 0, s, items, n_items, parts);
+  launch_k(COLI_K_CLIP_NORM, clip_norm_kernel, dim3(grid), dim3(kThreads), 0, s, items, n_items,
+           clip_item_from(kSumPast, n_items), parts);
   if (hipGetLastError() != hipSuccess) return COLI_E_HIP;
-  // From 128 MB on the partial sums are added up once: gradients in place that
-  // need no clipping take 109 us instead of 121 for 656 MB, 26 instead of 27 for
-  // 128 MB (16 MB: 11.5 against 9.2); clipped ones the same either way.
-  if (most < int64_t(128) << 20) {
+  if (n_items < kSumOnce) {
     launch_k(COLI_K_CLIP_SCALE, clip_scale_kernel, dim3((unsigned)n_items), dim3(kThreads), 0, s,
              items, (const double *)parts, grid, max_norm, norm);
     return hip_status(hipGetLastError());
@@ -382,12 +386,8 @@ int launch_clip(const coli_moe_clip_item_t *items, int64_t n_items, float max_no
   launch_k(COLI_K_CLIP_FINISH, clip_finish_kernel, dim3(1), dim3(kThreads), 0, s,
            (const double *)parts, grid, max_norm, norm);
   if (hipGetLastError() != hipSuccess) return COLI_E_HIP;
-  // Results that would not stay in the last cache anyway are read and written
-  // past it (656 MB: 222 us instead of 233; all of 256 MB 127 instead of 141, and
-  // 267 instead of 276 with an update from them behind; 128 MB 65 against 62).
-  launch_k(COLI_K_CLIP_SCALE,
-           most >= int64_t(256) << 20 ? clip_scale_many_kernel<true> : clip_scale_many_kernel<false>,
-           dim3((unsigned)n_items), dim3(kThreads), 0, s, items, (const float *)norm);
+  launch_k(COLI_K_CLIP_SCALE, clip_scale_many_kernel, dim3((unsigned)n_items), dim3(kThreads), 0, s,
+           items, clip_item_from(kScalePast, n_items), (const float *)norm);
   return hip_status(hipGetLastError());
 }
 

@@ -1,0 +1,104 @@
+"""How a clipping goes by the size of its plan: a host program evaluates
+csrc/clip_rules.h for the items that the library plans.  Needs no GPU, but for
+the last test."""
+import os
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+import int4_routed_expert_router_amd as coli
+from int4_routed_expert_router_amd import binding
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "int4_routed_expert_router_amd", "csrc")
+MB = 1 << 20
+FAKE = 1 << 32  # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def rules(tmp_path_factory):
+    """(bytes that the sum reads past the caches, bytes scaled past them, whether
+    the partial sums are added up once) of plans of (values, fp32)."""
+    d = tmp_path_factory.mktemp("rules")
+    (d / "rules.cpp").write_text('''
+#include <cstdio>
+#include "clip_rules.h"
+int main() {
+  long long items, sum = 0, scale = 0;
+  int n, f32;
+  if (std::scanf("%lld", &items) != 1) return 1;
+  while (std::scanf("%d %d", &n, &f32) == 2) {
+    const long long own = coli::clip_item_bytes(n, f32);
+    if (own >= coli::clip_item_from(coli::kSumPast, items)) sum += own;
+    if (own >= coli::clip_item_from(coli::kScalePast, items)) scale += own;
+  }
+  std::printf("%lld %lld %d", sum, scale, (int)(items >= coli::kSumOnce));
+}
+''')
+    exe = str(d / "rules")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-I", CSRC, str(d / "rules.cpp"), "-o", exe], check=True)
+
+    def run(sizes):
+        c, at = (binding._GradientC * len(sizes))(), FAKE
+        for i, (n, f32) in enumerate(sizes):
+            c[i] = binding._GradientC(at, at, n, f32, f32)
+            at += (n * (4 if f32 else 2) + 255) // 256 * 256
+        lib = binding.raw_library()
+        n = lib.coli_moe_clip_items(c, len(c))
+        items = (binding._ClipItemC * n)()
+        assert lib.coli_moe_clip_plan(c, len(c), items, n) == 0
+        text = "%d\n" % n + "".join("%d %d\n" % (i.n, i.dtypes & 1) for i in items)
+        out = subprocess.run([exe], input=text, check=True, capture_output=True, text=True).stdout
+        return n, tuple(int(v) for v in out.split())
+
+    return run
+
+
+@pytest.mark.parametrize("f32", [0, 1])
+def test_one_gradient_by_its_bytes(rules, f32):
+    for mb in (1, 16, 18, 32, 48, 63, 64, 65, 128, 255, 256, 257, 656):
+        _, (sum_past, scale_past, _) = rules([(mb * MB // (4 if f32 else 2), f32)])
+        item = 8192 * 4  # the last item may be a short one
+        assert sum_past == 0 if mb < 64 else sum_past > mb * MB - item, mb
+        assert scale_past == 0 if mb < 256 else scale_past > mb * MB - item, mb
+
+
+@pytest.mark.parametrize("n,each", [(5000, 300), (8192, 64), (4096, 256), (20000, 64), (2000, 2000),
+                                    (100000, 16)])
+def test_many_small_gradients_stay_in_the_caches(rules, n, each):
+    items, (sum_past, scale_past, once) = rules([(each, 1)] * n)
+    assert items == n and sum_past == scale_past == 0  # 0.5 to 16 MB
+    assert once == (n >= 4096)
+
+
+def test_a_large_gradient_among_small_ones(rules):
+    sizes = [(150 * MB // 4 * 4, 1)] + [(100, 0)] * 3000
+    _, (sum_past, scale_past, once) = rules(sizes)
+    assert 0.99 * 600 * MB < sum_past <= 600 * MB and once == 1
+    assert 0.99 * 600 * MB < scale_past <= 600 * MB
+    sizes = [(2 * MB, 1)] * 20 + [(6144, 1)] * 12  # 160 MB
+    _, (sum_past, scale_past, once) = rules(sizes)
+    assert 160 * MB < sum_past and scale_past == 0 and once == 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,each,launches", [(17, 100, 2), (4095, 16, 2), (4096, 16, 3), (5000, 300, 3)])
+def test_launches(n, each, launches):
+    g = torch.Generator(device="cuda").manual_seed(n)
+    flat = torch.randn(n * each, generator=g, device="cuda")
+    out = torch.full_like(flat, 7.0)
+    p = coli.Gradients(flat.split(each), out.split(each))
+    norm, ws = torch.empty(2, device="cuda"), coli.clip_workspace()
+    timer = coli.KernelTimer(8)
+    with timer:
+        coli.coli_moe_clip_gradients(p, 1.0, norm, ws)
+    torch.cuda.synchronize()
+    assert p.n == n and timer.c.count == launches
+    timer.close()
+    ref = float(flat.double().square().sum().sqrt())
+    got = norm.cpu().numpy()
+    # the norm is rounded once (and 1e-12 for the sums), the factor is a quotient of fp32
+    assert abs(got[0] - ref) <= ref * (2.0 ** -24 + 1e-12) and got[1] == np.float32(1) / got[0]
+    assert torch.equal(out, flat * norm[1])
