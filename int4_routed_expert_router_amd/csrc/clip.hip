@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kGroups = 1024;  // partial sums
-constexpr int kItem = 8192;    // values of an item, at most
+constexpr int kItem = 8192;    // values of an item, at most (and up to 7 in front of the first)
 constexpr int kFew = 16;       // items that one workgroup takes alone, a wave each
 enum { kGradF32 = 1, kOutF32 = 2 };
 

@@ -83,6 +83,34 @@ def test_a_large_gradient_among_small_ones(rules):
     assert 160 * MB < sum_past and scale_past == 0 and once == 1
 
 
+@pytest.mark.parametrize("f32,shift", [(0, 0), (0, 5), (1, 0), (1, 3)])
+@pytest.mark.parametrize("total", [1, 2047, 2048, 2049, 1 << 20, 4 * MB, 4 * MB + 2048, 8 * MB + 1,
+                                   16 * MB, 50 * MB])
+def test_sizes_of_items(total, f32, shift):
+    """Items are of a 2048th of all values, in whole 2048s and at most 8192, and a
+    gradient's first one is longer by what lies in front of 16 bytes."""
+    size = 4 if f32 else 2
+    parts = [total] if total < 4096 else [total - 1000, 999, 1]
+    c, at = (binding._GradientC * len(parts))(), FAKE
+    for i, n in enumerate(parts):
+        c[i] = binding._GradientC(at + size * shift, at + size * shift, n, f32, f32)
+        at += (n * size + 511) // 256 * 256
+    lib = binding.raw_library()
+    n = lib.coli_moe_clip_items(c, len(c))
+    items = (binding._ClipItemC * n)()
+    assert lib.coli_moe_clip_plan(c, len(c), items, n) == 0
+    per = min(max((total // 2048 + 2047) // 2048 * 2048, 2048), 8192)
+    front = 16 // size - shift if shift else 0
+    want = []
+    for left in parts:
+        want.append(min(left, per + front))
+        left -= want[-1]
+        while left:
+            want.append(min(left, per))
+            left -= want[-1]
+    assert [i.n for i in items] == want and max(want) <= 8192 + 7
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("n,each,launches", [(17, 100, 2), (4095, 16, 2), (4096, 16, 3), (5000, 300, 3)])
 def test_launches(n, each, launches):
