@@ -728,9 +728,9 @@ class Gradients:
         self.out = self.grads if out is None else list(out)
         if not self.grads or len(self.out) != len(self.grads):
             raise ValueError("%d gradients and %d outputs" % (len(self.grads), len(self.out)))
-        self._kept = [t.detach() for t in self.grads]
+        self._kept = [t.untyped_storage() for t in self.grads]
         if out is not None:
-            self._kept += [t.detach() for t in self.out]
+            self._kept += [t.untyped_storage() for t in self.out]
         dev = self.grads[0].get_device()
         c = (_GradientC * len(self.grads))()
         for i, (g, o) in enumerate(zip(self.grads, self.out)):
