@@ -282,9 +282,10 @@ __global__ void __launch_bounds__(B) norm_backward_kernel(NormBackArgs g) {
 
 // Sums n parts of H columns: COLS columns to a workgroup, every (1024 / COLS)th
 // part to COLS lanes, sixteen loads in flight.  16 columns keep the chip busy
-// up to H = 2048 (1,024 parts of 2048: 4.2 us with an empty launch's 3.9; 64
-// columns: 5.7), 64 read whole lines of wider ones (512 parts of 6144: 4.1
-// against 5.3).
+// with many parts of short rows (1,536 of 1024: 4.9 us with an empty launch's
+// 3.9; 64 columns 6.7), 64 read whole lines of long ones (256 of 16,384: 4.1
+// against 6.9).  In between, 768 parts of 2048, 512 of 4096 and 256 of 6144 take
+// 4.0 to 4.1 either way.
 template <int COLS>
 __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *__restrict__ parts, int n,
                                                            int H, float *__restrict__ out) {
