@@ -571,7 +571,8 @@ enum { COLI_NORM_PLAIN = 0, COLI_NORM_Q8_0 = 1, COLI_NORM_MXFP8 = 2 };
  * The norm is that of the stored s, so that a backward pass and later layers,
  * which see nothing else, agree with it; the codes are those of the bf16 y, so
  * that router and experts see the same values.  Sums are fp32; the sum of a
- * row's squares has to stay below 2^128.
+ * row's squares has to stay below 2^128, here and in the backward pass, and
+ * squares below 2^-126 lose bits (which shows where eps is as small).
  *  x [T*H] bf16;  residual, total [T*H] of residual_dtype (COLI_SRC_BF16 or
  *  _F32), both given or both NULL (total may be residual itself);
  *  y [T*H] bf16 or NULL (may be x itself);  format a COLI_NORM_*: q [T*H]
@@ -696,7 +697,8 @@ typedef struct coli_moe_clip_item {
 
 /* Plans a clipping of n gradients (n in [0, 2^20]) on the host: the number of
  * pieces, and the pieces themselves, which the caller copies to the device and
- * uses for as many calls as the gradients stay where they are.
+ * uses for as many calls as the gradients stay where they are.  It takes longer
+ * than a call (1 ms for 20,000 pieces), so gradients are best kept in place.
  * coli_moe_clip_items returns a negative COLI_E_* code for gradients that are
  * not valid; coli_moe_clip_plan writes exactly that many items. Host-only. */
 int64_t coli_moe_clip_items(const coli_moe_gradient_t *gradients, int32_t n);
@@ -709,8 +711,9 @@ size_t coli_moe_clip_workspace_bytes(void);
 /* The norm over all gradients of a plan, and clipping:
  *   norm[0] = sqrt(sum of all squares), the sum in 64 bits: no square
  *             overflows or vanishes
- *   norm[1] = max_norm / norm[0] where norm[0] > max_norm, else 1; 1 also where
- *             norm[0] is NaN or infinite, which the caller has to look for
+ *   norm[1] = max_norm / norm[0], in fp32, where norm[0] > max_norm, else 1; 1
+ *             also where norm[0] is NaN or infinite, which the caller has to
+ *             look for
  *   out = grad * norm[1], rounded to out's type
  * An out that is its grad is not touched where norm[1] is 1.
  *  items [n_items] device, 8-byte aligned, from coli_moe_clip_plan (n_items
